@@ -10,5 +10,10 @@ from .kda import (  # noqa: F401
     chunk_fwd,
     chunk_fwd_workspace_size,
     recurrent_step,
+    linear_chunk_fwd,
+    linear_chunk_bwd,
+    linear_recurrent_step,
+    qk_norm_rope,
+    qk_norm_rope_bwd,
     library_path,
 )

@@ -1,0 +1,134 @@
+// kda_linear.cuh -- definitions shared by the files of the linear attention with
+// one fixed decay per head: how its forward and its three gradients map onto one
+// recurrence, how sequences are cut into segments, and the launchers.
+//
+// With lambda = e^l per head, scale s = dk^{-1/2} and states of dk x dv:
+//
+//   S_t = lambda S_{t-1} + k_t v_t^T,   o_t = s S_t^T q_t                    (forward)
+//   dq_t = s S_t d_o_t                                                       (first to last token)
+//   G_t = lambda G_{t+1} + s q_t d_o_t^T, dk_t = G_t v_t, dv_t = G_t^T k_t   (last to first token)
+//
+// where G_T also holds the cotangent of the final state.  Every line has the form
+//
+//   Z_t = lambda Z_{t-1} + c_upd b_t c_t^T,   y_t = (read weight) Z_t^T a_t
+//
+// in its own direction, with (a, b, c, y) = (q, k, v, o), (d_o, v, k, dq),
+// (v, d_o, q, dk), (k, q, d_o, dv) and Z = S, S^T, G^T, G.  LinRole names one line.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+constexpr int kLinChunk = 128;    // tokens per chunk: the rows of one tensor-core tile
+constexpr int kLinMaxRoles = 3;
+
+struct LinRole {
+    int a, b, c;            // LinArgs::x indices of the query-, key- and value-like inputs
+    void* y;                // output [tokens, H, D2], input dtype
+    const float* s_in;      // state before the first processed token, nullable (zeros)
+    float* s_out;           // state after the last one, nullable
+    float* seg;             // [segments][H][D1 * D2]: each segment's own sum, then its entering state
+    bool transposed;        // Z is the transpose of the user's [dk, dv] states
+    bool reverse;           // from the last token to the first
+    float c_inter, c_intra; // y_t = c_inter lambda^.. Z_0^T a_t + c_intra sum_i lambda^.. <a_t, b_i> c_i
+    float c_upd;
+};
+
+// Where the segments lie.  Sequences are B rows of T tokens, or packed by cu.
+// A segment is a run of seg_tok tokens of one sequence (its last one may be
+// short; a sequence without tokens has one empty segment).  With one segment per
+// sequence a single pass over the tokens does all; otherwise a pass over keys and
+// values first sums every segment's own contribution to the state, and a scan
+// turns those into the states that enter each segment, so that all segments run
+// at the same time.
+// Packed sequences: tab = [seg_tok][first segment of the r-th sequence, r = 0..N]
+// [r-th sequence], longest first, so that long segments start first.
+struct LinMap {
+    const int32_t* cu;
+    const int32_t* tab;
+    int N, T;               // T: tokens per sequence, or in all when packed
+    int seg_tok, num_seg;   // not packed: tokens per segment, segments per sequence
+
+    struct Seg {
+        int seq, begin, len;      // sequence, first token in the flat token order, tokens
+        int index, count;         // which segment of how many of its sequence
+    };
+    __device__ __forceinline__ int segments() const { return cu ? tab[1 + N] : N * num_seg; }
+    __device__ __forceinline__ void range(int r, int& seq, int& first, int& count) const {   // r-th sequence's segments
+        if (!cu) {
+            seq = r; first = r * num_seg; count = num_seg;
+            return;
+        }
+        seq = tab[2 + N + r]; first = tab[1 + r]; count = tab[2 + r] - first;
+    }
+    __device__ __forceinline__ Seg locate(int s) const {
+        Seg g;
+        int first, seq_begin, seq_len, size;
+        if (!cu) {
+            g.seq = s / num_seg; first = g.seq * num_seg;
+            g.count = num_seg;
+            seq_begin = g.seq * T; seq_len = T; size = seg_tok;
+        } else {
+            int lo = 0, hi = N - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (tab[1 + mid] <= s) lo = mid; else hi = mid - 1;
+            }
+            range(lo, g.seq, first, g.count);
+            seq_begin = cu[g.seq]; seq_len = cu[g.seq + 1] - seq_begin; size = tab[0];
+        }
+        g.index = s - first;
+        const int off = g.index * size;          // < seq_len + size, see the host's check of T
+        g.begin = seq_begin + off;
+        g.len = min(size, seq_len - off);
+        return g;
+    }
+};
+
+struct LinArgs {
+    const void* x[4];             // inputs the roles name: q, k, v, d_o
+    int dim[4];                   // channels of each
+    const float* log_decay;       // [H], nullable (no decay)
+    int H, dk, dv;
+    int64_t tokens;               // in all
+    bool bf16;
+    LinMap map;
+    int max_segments;             // host bound on map.segments()
+    bool split;                   // some sequence may have more than one segment
+    int roles;
+    LinRole role[kLinMaxRoles];
+    WsHeader* hdr;
+    cudaStream_t stream;
+};
+
+// Powers of a head's decay: e^(l n), from a 64-bit exponent; l is kept finite so
+// that l n is 0 at n = 0 also for l = -inf (a state forgotten at every token).
+__device__ __forceinline__ double lin_log_decay(const float* log_decay, int h) {
+    if (!log_decay) return 0.0;
+    const float l = log_decay[h];
+    return l < -1e30f ? -1e30 : (double)l;
+}
+__device__ __forceinline__ float lin_pow(double l, int n) { return (float)exp(l * (double)n); }
+
+cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens);
+cudaError_t launch_linear_scan(const LinArgs& a);
+cudaError_t launch_linear_simt(const LinArgs& a, bool states_only);
+cudaError_t launch_linear_tc(const LinArgs& a, bool states_only);
+
+struct LinStepArgs {
+    const void* q; const void* k; const void* v;
+    const float* log_decay;       // [H], nullable
+    float* state; void* o;
+    int B, H, dk, dv;
+    bool bf16;
+    float scale;
+    cudaStream_t stream;
+};
+cudaError_t launch_linear_step(const LinStepArgs& a);
+
+}  // namespace kda

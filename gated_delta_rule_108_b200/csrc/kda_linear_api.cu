@@ -1,0 +1,276 @@
+// kda_linear_api.cu -- the C entry points of the linear attention with one fixed
+// decay per head (declared in include/kda.h): argument checks, the plan of
+// segments, the workspace, the launches.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/kda.h"
+#include "kda_linear.cuh"
+#include "kda_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int kSms = 148;   // the plan and the workspace size are those of one B200
+
+template <typename... A>
+kda_status fail(kda_status st, const char* fmt, A... args) {
+    return (kda_status)set_error(st, fmt, args...);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool supported_dim(int d) { return d == 64 || d == 128; }
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Into how many segments a sequence of `chunks` chunks is cut, when `chains`
+// CTAs work on each segment number: the cheapest by the count of waves.  In units
+// of one chunk of the chunk kernel, a chunk of the summing pass costs 0.55, a CTA
+// 0.8 to start and end, and the two extra launches 2.5 together.
+int plan_segment_chunks(int64_t chains, int64_t chunks) {
+    if (chunks <= 1) return 1;
+    double best = 0;
+    int64_t best_len = chunks;
+    for (int64_t s = 1; s <= std::min<int64_t>(chunks, 96); ++s) {
+        const int64_t len = (chunks + s - 1) / s, n = (chunks + len - 1) / len;
+        const double waves = std::ceil((double)(chains * n) / kSms), sums = std::ceil((double)(chains * (n - 1)) / kSms);
+        const double cost = waves * (len + 0.8) + (n > 1 ? sums * (0.55 * len + 0.8) + 2.5 : 0.0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            best_len = len;
+        }
+    }
+    return (int)best_len;
+}
+
+struct Plan {
+    int N, seg_tok, num_seg, max_segments, balance_tokens;
+    bool split;
+    size_t tab_off, seg_off, seg_bytes, total;   // seg_bytes: one role's segment states
+};
+
+bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, kda_dtype dtype, int roles, Plan& p) {
+    if (B < 0 || T < 0 || H <= 0 || !supported_dim(dk) || !supported_dim(dv)) return false;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return false;
+    if (varlen && (B != 1 || num_seqs < 0)) return false;
+    if ((int64_t)B * T >= (int64_t)1 << 30 || H > 65535 || (varlen ? num_seqs : B) >= 1 << 24) return false;
+    p.N = varlen ? num_seqs : B;
+    // CTAs per segment and head: the CUDA-core kernel takes 64 value columns each
+    const int64_t per_head = (int64_t)roles * (dtype == KDA_BF16 ? 1 : std::max(dk, dv) / 64);
+    const int64_t chunks = ((int64_t)T + kLinChunk - 1) / kLinChunk;
+    const int64_t chains = per_head * H * (varlen ? 1 : std::max(B, 1));
+    const int len = plan_segment_chunks(chains, chunks);
+    p.seg_tok = std::max(len, 1) * kLinChunk;
+    p.num_seg = std::max<int>(1, (int)((chunks + len - 1) / std::max(len, 1)));
+    p.split = p.num_seg > 1;
+    // packed: every sequence may end in a short segment; unsplit when the longest
+    // is within 1.6 times one SM's share (the summing pass would cost 0.6 of it)
+    const int64_t most = varlen ? (int64_t)p.N + T / p.seg_tok : (int64_t)p.N * p.num_seg;
+    if (most * H * per_head >= (int64_t)1 << 31) return false;
+    p.max_segments = (int)most;
+    p.balance_tokens = (int)std::min<int64_t>((int64_t)1 << 30, (int64_t)(1.6 * (double)T * H * per_head / kSms));
+    if (!p.split) p.balance_tokens = 1 << 30;
+    p.tab_off = kHeaderBytes;
+    p.seg_off = round_up(p.tab_off + (varlen ? sizeof(int32_t) * (2 * (size_t)p.N + 2) : 0), 256);
+    p.seg_bytes = p.split ? sizeof(float) * (size_t)p.max_segments * H * dk * dv : 0;
+    p.total = round_up(p.seg_off + p.seg_bytes * roles, 256);
+    return true;
+}
+
+kda_status check_sizes(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, kda_dtype dtype, int roles, Plan& p) {
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (B < 0 || T < 0 || H <= 0) return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%d T=%d H=%d", B, T, H);
+    if (dk <= 0 || dv <= 0) return fail(KDA_ERR_INVALID_ARG, "bad head sizes dk=%d dv=%d", dk, dv);
+    if (!supported_dim(dk) || !supported_dim(dv))
+        return fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d not in {64, 128}", dk, dv);
+    if (varlen && B != 1) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens requires B == 1 (got B=%d)", B);
+    if (varlen && num_seqs < 0) return fail(KDA_ERR_INVALID_ARG, "num_seqs=%d < 0", num_seqs);
+    if (!make_plan(B, T, H, dk, dv, num_seqs, varlen, dtype, roles, p))
+        return fail(KDA_ERR_UNSUPPORTED, "B=%d T=%d H=%d num_seqs=%d is too large", B, T, H, num_seqs);
+    return KDA_OK;
+}
+
+kda_status check_workspace(void* workspace, size_t bytes, size_t need) {
+    if (!workspace) return fail(KDA_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (bytes < need) return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", bytes, need);
+    return KDA_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const char *x = (const char*)a, *y = (const char*)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, int B, int T, int H, int dk, int dv,
+                    kda_dtype dtype, void* workspace, void* stream) {
+    LinArgs a{};
+    char* ws = static_cast<char*>(workspace);
+    a.log_decay = log_decay;
+    a.H = H; a.dk = dk; a.dv = dv;
+    a.tokens = (int64_t)B * T;
+    a.bf16 = dtype == KDA_BF16;
+    a.map.cu = cu;
+    a.map.tab = cu ? reinterpret_cast<int32_t*>(ws + p.tab_off) : nullptr;
+    a.map.N = p.N; a.map.T = T; a.map.seg_tok = p.seg_tok; a.map.num_seg = p.num_seg;
+    a.max_segments = p.max_segments;
+    a.split = p.split;
+    a.hdr = static_cast<WsHeader*>(workspace);
+    a.stream = static_cast<cudaStream_t>(stream);
+    return a;
+}
+
+// All roles of `a`; those with the same (D1, D2) share a launch.
+cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
+    LinArgs all = a;
+    for (int i = 0; i < all.roles; ++i)
+        all.role[i].seg = p.split ? reinterpret_cast<float*>(ws + p.seg_off + p.seg_bytes * i) : nullptr;
+    cudaError_t e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
+    if (p.max_segments == 0) return e;
+    auto pass = [&](bool states_only) {
+        bool done[kLinMaxRoles] = {};
+        for (int i = 0; i < all.roles && e == cudaSuccess; ++i) {
+            if (done[i]) continue;
+            LinArgs one = all;
+            one.roles = 0;
+            for (int j = i; j < all.roles; ++j)
+                if (all.dim[all.role[j].a] == all.dim[all.role[i].a] && all.dim[all.role[j].c] == all.dim[all.role[i].c]) {
+                    one.role[one.roles++] = all.role[j];
+                    done[j] = true;
+                }
+            e = a.bf16 ? launch_linear_tc(one, states_only) : launch_linear_simt(one, states_only);
+        }
+    };
+    if (p.split && e == cudaSuccess) {
+        pass(true);
+        if (e == cudaSuccess) e = launch_linear_scan(all);
+    }
+    if (e == cudaSuccess) pass(false);
+    return e;
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int varlen, kda_dtype dtype) {
+    Plan p;
+    return make_plan(B, T, H, dk, dv, num_seqs, varlen != 0, dtype, 1, p) ? p.total : 0;
+}
+
+size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int varlen, kda_dtype dtype) {
+    Plan p;
+    return make_plan(B, T, H, dk, dv, num_seqs, varlen != 0, dtype, 3, p) ? p.total : 0;
+}
+
+kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                const float* initial_state, const int32_t* cu_seqlens, int B, int T, int H, int dk,
+                                int dv, int num_seqs, kda_dtype dtype, void* o, float* final_state, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    Plan p;
+    kda_status st = check_sizes(B, T, H, dk, dv, num_seqs, cu_seqlens != nullptr, dtype, 1, p);
+    if (st != KDA_OK) return st;
+    if ((int64_t)B * T > 0) {
+        if (!q || !k || !v || !o) return fail(KDA_ERR_INVALID_ARG, "null input/output pointer");
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+            return fail(KDA_ERR_INVALID_ARG, "q/k/v/o must be 16-byte aligned");
+    }
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * T * H * dk * es, vbytes = (size_t)B * T * H * dv * es;
+    if (overlap(o, vbytes, q, kbytes) || overlap(o, vbytes, k, kbytes) || overlap(o, vbytes, v, vbytes))
+        return fail(KDA_ERR_INVALID_ARG, "o overlaps an input");
+    if (!aligned16(initial_state)) return fail(KDA_ERR_INVALID_ARG, "initial_state misaligned");
+    if (!aligned16(final_state)) return fail(KDA_ERR_INVALID_ARG, "final_state misaligned");
+    const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
+    if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "initial_state and final_state overlap without being equal");
+    st = check_workspace(workspace, workspace_bytes, p.total);
+    if (st != KDA_OK) return st;
+
+    LinArgs a = common_args(p, log_decay, cu_seqlens, B, T, H, dk, dv, dtype, workspace, stream);
+    const void* x[4] = {q, k, v, nullptr};
+    const int dims[4] = {dk, dk, dv, dv};
+    for (int i = 0; i < 4; ++i) { a.x[i] = x[i]; a.dim[i] = dims[i]; }
+    const float s = 1.0f / sqrtf((float)dk);
+    a.roles = 1;
+    a.role[0] = {0, 1, 2, o, initial_state, final_state, nullptr, false, false, s, s, 1.f};
+    const cudaError_t e = run_roles(a, p, static_cast<char*>(workspace));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_chunk_fwd launch failed: %s", cudaGetErrorString(e));
+    return fail(KDA_OK, "");
+}
+
+kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                const float* initial_state, const int32_t* cu_seqlens, const void* d_o,
+                                const float* d_final_state, int B, int T, int H, int dk, int dv, int num_seqs,
+                                kda_dtype dtype, void* dq, void* dk_out, void* dv_out, float* d_initial_state,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    Plan p;
+    kda_status st = check_sizes(B, T, H, dk, dv, num_seqs, cu_seqlens != nullptr, dtype, 3, p);
+    if (st != KDA_OK) return st;
+    if ((int64_t)B * T > 0) {
+        if (!q || !k || !v || !d_o || !dq || !dk_out || !dv_out) return fail(KDA_ERR_INVALID_ARG, "null input/output pointer");
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk_out) ||
+            !aligned16(dv_out))
+            return fail(KDA_ERR_INVALID_ARG, "q/k/v/d_o/dq/dk/dv must be 16-byte aligned");
+    }
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * T * H * dk * es, vbytes = (size_t)B * T * H * dv * es;
+    const void* in[4] = {q, k, v, d_o};
+    const size_t in_bytes[4] = {kbytes, kbytes, vbytes, vbytes};
+    for (int i = 0; i < 4; ++i)
+        if (overlap(dq, kbytes, in[i], in_bytes[i]) || overlap(dk_out, kbytes, in[i], in_bytes[i]) ||
+            overlap(dv_out, vbytes, in[i], in_bytes[i]))
+            return fail(KDA_ERR_INVALID_ARG, "a gradient overlaps an input");
+    if (!aligned16(initial_state)) return fail(KDA_ERR_INVALID_ARG, "initial_state misaligned");
+    if (!aligned16(d_final_state)) return fail(KDA_ERR_INVALID_ARG, "d_final_state misaligned");
+    if (!aligned16(d_initial_state)) return fail(KDA_ERR_INVALID_ARG, "d_initial_state misaligned");
+    const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
+    if (overlap(initial_state, state_bytes, d_initial_state, state_bytes) ||
+        overlap(d_final_state, state_bytes, d_initial_state, state_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "d_initial_state overlaps an input state");
+    st = check_workspace(workspace, workspace_bytes, p.total);
+    if (st != KDA_OK) return st;
+
+    LinArgs a = common_args(p, log_decay, cu_seqlens, B, T, H, dk, dv, dtype, workspace, stream);
+    const void* x[4] = {q, k, v, d_o};
+    const int dims[4] = {dk, dk, dv, dv};
+    for (int i = 0; i < 4; ++i) { a.x[i] = x[i]; a.dim[i] = dims[i]; }
+    const float s = 1.0f / sqrtf((float)dk);
+    a.roles = 3;
+    a.role[0] = {3, 2, 1, dq, initial_state, nullptr, nullptr, true, false, s, s, 1.f};
+    a.role[1] = {2, 3, 0, dk_out, d_final_state, nullptr, nullptr, true, true, 1.f, s, s};
+    a.role[2] = {1, 0, 3, dv_out, d_final_state, d_initial_state, nullptr, false, true, 1.f, s, s};
+    const cudaError_t e = run_roles(a, p, static_cast<char*>(workspace));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_chunk_bwd launch failed: %s", cudaGetErrorString(e));
+    return fail(KDA_OK, "");
+}
+
+kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v, const float* log_decay,
+                                     float* state_inout, int B, int H, int dk, int dv, kda_dtype dtype, void* o,
+                                     void* stream) {
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (B < 0 || H <= 0 || dk <= 0 || dv <= 0)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%d H=%d dk=%d dv=%d", B, H, dk, dv);
+    if (!supported_dim(dk) || !supported_dim(dv))
+        return fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d not in {64, 128}", dk, dv);
+    if ((int64_t)B * H >= (int64_t)1 << 28) return fail(KDA_ERR_UNSUPPORTED, "state too large");
+    if (B > 0) {
+        if (!q || !k || !v || !state_inout || !o) return fail(KDA_ERR_INVALID_ARG, "null pointer");
+        if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state_inout) || !aligned16(o))
+            return fail(KDA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+        if (overlap(o, (size_t)B * H * dv * (dtype == KDA_BF16 ? 2 : 4), state_inout, (size_t)B * H * dk * dv * 4))
+            return fail(KDA_ERR_INVALID_ARG, "o aliases state_inout");
+    }
+    LinStepArgs a{};
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.state = state_inout; a.o = o;
+    a.B = B; a.H = H; a.dk = dk; a.dv = dv;
+    a.bf16 = dtype == KDA_BF16;
+    a.scale = 1.0f / sqrtf((float)dk);
+    a.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_linear_step(a);
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_recurrent_step launch failed: %s", cudaGetErrorString(e));
+    return fail(KDA_OK, "");
+}
+
+}  // extern "C"

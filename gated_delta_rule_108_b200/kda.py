@@ -7,6 +7,7 @@ is no CPU path: if the library is missing, every call raises :class:`KDAError`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -24,6 +25,7 @@ _STATUS = {
 }
 KDA_F32, KDA_BF16 = 0, 1
 KDA_GATE_CHANNEL, KDA_GATE_HEAD, KDA_GATE_NONE = 0, 1, 2
+KDA_NORM_RMS, KDA_NORM_L2 = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -75,6 +77,24 @@ def _declare(lib):
     lib.kda_chunk_bwd_saved.restype = i
     lib.kda_chunk_bwd_saved.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
                                         vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for name in ("kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_bwd_workspace_size"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i, i, i, i, i, i, i, i]
+    lib.kda_linear_chunk_fwd.restype = i
+    lib.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, vp, sz, vp]
+    lib.kda_linear_chunk_bwd.restype = i
+    lib.kda_linear_chunk_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i,
+                                         vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_linear_recurrent_step.restype = i
+    lib.kda_linear_recurrent_step.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
+    ip = ctypes.POINTER(ctypes.c_int64)
+    lib.kda_qk_norm_rope.restype = i
+    lib.kda_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ip, ip, i, i, f, i, vp, vp, vp]
+    lib.kda_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.kda_qk_norm_rope_bwd.restype = i
+    lib.kda_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ip, ip, i, i, f, i,
+                                         vp, vp, vp, vp, vp, sz, vp]
     lib.kda_workspace_status.restype = i
     lib.kda_workspace_status.argtypes = [vp, sz, vp]
     lib.kda_set_stage_events.restype = i
@@ -425,3 +445,277 @@ def recurrent_step(q, k, v, log_alpha, beta, state, o=None, stream=None) -> torc
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(state),
         B, H, dk, dv, _dtype_code(q), gate, _ptr(o), _stream_ptr(stream, q.device)))
     return o
+
+
+# ------------------------------------------- linear attention, decay per head --
+def _on(device):
+    """The library launches on the current device; make that the tensors' device
+    for the call where it is another."""
+    return (contextlib.nullcontext() if torch.cuda.current_device() == device.index
+            else torch.cuda.device(device))
+
+
+def _log_decay(log_decay, H: int, device) -> None:
+    if log_decay is not None:
+        _shape(log_decay, "log_decay", (H,))
+        _need(log_decay, "log_decay", torch.float32, device)
+
+
+def linear_chunk_fwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
+                                    num_seqs: int, varlen: bool, dtype: torch.dtype) -> int:
+    """Workspace bytes ``linear_chunk_fwd`` needs (``kda_linear_chunk_fwd_workspace_size``)."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, num_seqs, int(bool(varlen)), code))
+
+
+def linear_chunk_bwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
+                                    num_seqs: int, varlen: bool, dtype: torch.dtype) -> int:
+    """Workspace bytes ``linear_chunk_bwd`` needs (``kda_linear_chunk_bwd_workspace_size``)."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, num_seqs, int(bool(varlen)), code))
+
+
+def linear_chunk_fwd(q, k, v, log_decay=None, initial_state=None, cu_seqlens=None,
+                     output_final_state: bool = True, o=None, final_state=None, workspace=None,
+                     stream=None, check: Optional[bool] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with one fixed decay per head, chunkwise (``kda_linear_chunk_fwd``):
+    S_t = e^log_decay S_{t-1} + k_t v_t^T, o_t = dk^-1/2 S_t^T q_t.
+
+    q, k [B, T, H, dk]; v [B, T, H, dv]; log_decay [H] fp32 or None (no decay);
+    initial_state [N, H, dk, dv] fp32 or None; cu_seqlens int32 [N+1] or None.
+    Returns (o [B, T, H, dv], final_state [N, H, dk, dv] or None).  The decays
+    are constants: they get no gradient.  ``check`` as in :func:`chunk_fwd`.
+    """
+    _dims(q, "q", 4)
+    _dims(v, "v", 4)
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    N = _num_seqs(B, cu_seqlens)
+    for t, n, shape in ((k, "k", (B, T, H, dk)), (v, "v", (B, T, H, dv)),
+                        (initial_state, "initial_state", (N, H, dk, dv)), (o, "o", (B, T, H, dv)),
+                        (final_state, "final_state", (N, H, dk, dv))):
+        _shape(t, n, shape)
+    dev = q.device
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, q.dtype, dev)
+    _log_decay(log_decay, H, dev)
+    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (initial_state, "initial_state", torch.float32),
+                     (o, "o", q.dtype), (final_state, "final_state", torch.float32),
+                     (workspace, "workspace", None)):
+        if t is not None:
+            _need(t, n, dt, dev)
+    code = _dtype_code(q)
+    made = []
+    if o is None:
+        o = torch.empty(B, T, H, dv, dtype=q.dtype, device=dev)
+        made.append(o)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
+        made.append(final_state)
+    if workspace is None:
+        ws_bytes = linear_chunk_fwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, q.dtype)
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _used_on(stream, dev, *made)
+    with _on(dev):
+        _check(lib().kda_linear_chunk_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(cu_seqlens),
+            B, T, H, dk, dv, N, code, _ptr(o), _ptr(final_state),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
+        if check if check is not None else _validate_default():
+            _check_device_status(workspace, stream)
+    return o, final_state
+
+
+def linear_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=None, cu_seqlens=None,
+                     output_d_initial_state: bool = True, workspace=None, stream=None,
+                     check: Optional[bool] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of :func:`linear_chunk_fwd` (``kda_linear_chunk_bwd``).
+
+    Inputs as ``linear_chunk_fwd``; d_o like o; d_final_state [N, H, dk, dv] fp32
+    or None.  Returns a dict with dq, dk, dv (input dtype) and dS0 [N, H, dk, dv]
+    (fp32, or None when ``output_d_initial_state`` is false).
+    """
+    _dims(q, "q", 4)
+    _dims(v, "v", 4)
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    N = _num_seqs(B, cu_seqlens)
+    for t, n, shape in ((k, "k", (B, T, H, dk)), (v, "v", (B, T, H, dv)), (d_o, "d_o", (B, T, H, dv)),
+                        (initial_state, "initial_state", (N, H, dk, dv)),
+                        (d_final_state, "d_final_state", (N, H, dk, dv))):
+        _shape(t, n, shape)
+    dev = q.device
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
+        _need(t, n, q.dtype, dev)
+    _log_decay(log_decay, H, dev)
+    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (initial_state, "initial_state", torch.float32),
+                     (d_final_state, "d_final_state", torch.float32), (workspace, "workspace", None)):
+        if t is not None:
+            _need(t, n, dt, dev)
+    code = _dtype_code(q)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dS0": (torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
+                 if output_d_initial_state else None)}
+    made = list(g.values())
+    if workspace is None:
+        ws_bytes = linear_chunk_bwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, q.dtype)
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _used_on(stream, dev, *made)
+    with _on(dev):
+        _check(lib().kda_linear_chunk_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_o),
+            _ptr(d_final_state), B, T, H, dk, dv, N, code, _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
+            _ptr(g["dS0"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream_ptr(stream, dev)))
+        if check if check is not None else _validate_default():
+            _check_device_status(workspace, stream)
+    return g
+
+
+def linear_recurrent_step(q, k, v, log_decay, state, o=None, stream=None) -> torch.Tensor:
+    """One token of :func:`linear_chunk_fwd`'s recurrence (``kda_linear_recurrent_step``);
+    ``state`` is updated in place.
+
+    q, k [B, H, dk]; v [B, H, dv]; log_decay [H] fp32 or None; state [B, H, dk, dv]
+    fp32.  Returns o [B, H, dv] in q's dtype.
+    """
+    _dims(q, "q", 3)
+    _dims(v, "v", 3)
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    for t, n, shape in ((k, "k", (B, H, dk)), (v, "v", (B, H, dv)), (state, "state", (B, H, dk, dv)),
+                        (o, "o", (B, H, dv))):
+        _shape(t, n, shape)
+    dev = q.device
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, q.dtype, dev)
+    _log_decay(log_decay, H, dev)
+    _need(state, "state", torch.float32, dev)
+    code = _dtype_code(q)
+    if o is not None:
+        _need(o, "o", q.dtype, dev)
+    else:
+        o = torch.empty(B, H, dv, dtype=q.dtype, device=dev)
+        _used_on(stream, dev, o)
+    with _on(dev):
+        _check(lib().kda_linear_recurrent_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), B, H, dk, dv, code, _ptr(o),
+            _stream_ptr(stream, dev)))
+    return o
+
+
+# ------------------------------------------------ norm and rotation of q and k --
+def _need_rows(t: torch.Tensor, name: str, dtype, device):
+    """Like :func:`_need` for rows that may lie apart: only channels are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+
+
+def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm, cotangents=()):
+    """Checks the arguments the norm and its gradients share; returns the sizes
+    (B, T, Hq, Hk, d, rotary_dim), the norm's code and the strides."""
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(q.shape)}")
+    _dims(k, "k", q.dim())
+    lead, Hq, d = tuple(q.shape[:-2]), q.shape[-2], q.shape[-1]
+    Hk = k.shape[-2]
+    _shape(k, "k", (*lead, Hk, d))
+    B, T = lead if q.dim() == 4 else (lead[0], 1)
+    for t, n, shape in ((q_weight, "q_weight", (d,)), (k_weight, "k_weight", (d,)), (positions, "positions", lead),
+                        *cotangents):
+        _shape(t, n, shape)
+    rot = 0
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", 1)
+        rot = 2 * inv_freq.numel()
+        if q.dim() == 3 and positions is None:
+            raise ValueError("a rotation of single tokens needs their positions")
+    if norm not in ("rms", "l2"):
+        raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
+    dev = q.device
+    _need_rows(q, "q", q.dtype, dev)
+    _need_rows(k, "k", q.dtype, dev)
+    for t, n, dt in ((q_weight, "q_weight", torch.float32), (k_weight, "k_weight", torch.float32),
+                     (inv_freq, "inv_freq", torch.float32), (positions, "positions", torch.int32)):
+        if t is not None:
+            _need(t, n, dt, dev)
+
+    def strides(t):
+        s = t.stride() if t.dim() == 4 else (t.stride(0), 0, t.stride(1))
+        # a dimension of one element is never stepped over, whatever stride torch gives it
+        return (ctypes.c_int64 * 3)(*[0 if n == 1 else x for x, n in zip(s, (B, T, t.shape[-2]))])
+
+    return (B, T, Hq, Hk, d, rot), (KDA_NORM_RMS if norm == "rms" else KDA_NORM_L2), strides(q), strides(k)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, norm: str = "l2",
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Norm of queries and keys per head and position rotation in one pass
+    (``kda_qk_norm_rope``), as they go into the attention calls of this module.
+
+    q [B, T, Hq, d], k [B, T, Hk, d] (or single tokens [B, Hq, d], [B, Hk, d]),
+    which may be slices of a joint projection; ``norm`` "l2" (unit rows) or "rms";
+    q_weight, k_weight [d] fp32 or None; inv_freq [rotary_dim / 2] fp32 turns the
+    first rotary_dim channels by position * inv_freq (None: no rotation), in pairs
+    (j, j + rotary_dim / 2) or, with ``interleaved``, (2j, 2j + 1); positions int32
+    [B, T] ([B] for single tokens), None: 0 .. T-1.  Returns (q_out, k_out),
+    contiguous and of the inputs' dtype.
+    """
+    shapes = (((*q.shape,), q_out, "q_out"), ((*k.shape,), k_out, "k_out"))
+    (B, T, Hq, Hk, d, rot), code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
+                                                      [(t, n, s) for s, t, n in shapes])
+    dev, dt = q.device, _dtype_code(q)
+    made = []
+    for s, t, n in shapes:
+        if t is not None:
+            _need(t, n, q.dtype, dev)
+        else:
+            made.append(torch.empty(s, dtype=q.dtype, device=dev))
+    _used_on(stream, dev, *made)
+    k_out = made.pop() if k_out is None else k_out
+    q_out = made.pop() if q_out is None else q_out
+    with _on(dev):
+        _check(lib().kda_qk_norm_rope(
+            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), B, T, Hq, Hk, d, rot,
+            qs, ks, dt, code, float(eps), int(bool(interleaved)), _ptr(q_out), _ptr(k_out), _stream_ptr(stream, dev)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, inv_freq=None, positions=None,
+                     norm: str = "l2", eps: float = 1e-6, interleaved: bool = False, workspace=None,
+                     stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of :func:`qk_norm_rope` (``kda_qk_norm_rope_bwd``): q, k its inputs,
+    d_q_out, d_k_out the cotangents of its outputs.  Returns a dict with dq, dk
+    (contiguous) and dq_weight, dk_weight [d] fp32 (None without that weight)."""
+    (B, T, Hq, Hk, d, rot), code, qs, ks = _norm_args(
+        q, k, q_weight, k_weight, inv_freq, positions, norm,
+        [(d_q_out, "d_q_out", tuple(q.shape)), (d_k_out, "d_k_out", tuple(k.shape))])
+    dev, dt = q.device, _dtype_code(q)
+    for t, n in ((d_q_out, "d_q_out"), (d_k_out, "d_k_out")):
+        _need(t, n, q.dtype, dev)
+    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+         "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+         "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
+    made = list(g.values())
+    if workspace is not None:
+        _need(workspace, "workspace", None, dev)
+    elif q_weight is not None or k_weight is not None:
+        workspace = torch.empty(max(int(lib().kda_qk_norm_rope_bwd_workspace_size(d)), 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _used_on(stream, dev, *made)
+    with _on(dev):
+        _check(lib().kda_qk_norm_rope_bwd(
+            _ptr(q), _ptr(k), _ptr(d_q_out), _ptr(d_k_out), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+            _ptr(positions), B, T, Hq, Hk, d, rot, qs, ks, dt, code, float(eps), int(bool(interleaved)),
+            _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
+    return g

@@ -326,6 +326,133 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
                                size_t workspace_bytes, void* stream);
 
 /*
+ * Linear attention with one fixed decay per head: the recurrence above without
+ * the prediction and with a decay that is a constant of the head,
+ *
+ *     S_t = lambda S_{t-1} + k_t v_t^T,    o_t = d_k^{-1/2} S_t^T q_t,    lambda = e^{log_decay[h]},
+ *
+ * chunkwise over whole sequences.  Written out, o_t = d_k^{-1/2} (sum_{i <= t}
+ * lambda^{t-i} <q_t, k_i> v_i + lambda^{t+1} S_0^T q_t).  Such decays are set per
+ * head when a model is built (fast heads next to slow ones) and are not trained,
+ * so they have no gradient.
+ *
+ *  q, k        [B, T, H, dk]   dtype
+ *  v           [B, T, H, dv]   dtype
+ *  log_decay   [H]             fp32, <= 0; -inf forgets everything at each token;
+ *              NULL: no decay (lambda = 1)
+ *  initial_state, cu_seqlens, final_state, o, sizes: as kda_chunk_fwd (sequences
+ *              may be empty: their final state is their initial state); o must
+ *              not overlap an input
+ *  workspace   at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
+ *              aligned; its contents on entry do not matter.  Calls that share
+ *              one workspace must be ordered on one stream.
+ *              kda_workspace_status reads its status (KDA_ERR_BAD_SEQLENS,
+ *              KDA_ERR_TIMEOUT).
+ *
+ * A sequence that is long for the number of heads and sequences is cut into
+ * segments that run at the same time: one pass over k and v sums what each
+ * segment adds to the state, a scan joins the sums, and the chunk kernel runs on
+ * all segments with their entering states.  B*T < 2^30.
+ *
+ * Numerics: bf16 inputs use the tensor cores with bf16 operands and fp32
+ * accumulation; o differs from the exact result by about 1.4 times its own
+ * rounding at most, and the states keep fp32 (the factors that enter them are
+ * split into three bf16 parts).  fp32 inputs are computed in fp32 on CUDA cores.
+ * Inputs must be finite: an infinity or a NaN at one token reaches every output
+ * of its chunk of 128 tokens, also those before it.  It does not reach other
+ * sequences.
+ */
+size_t kda_linear_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv,
+                                           int num_seqs, int varlen, kda_dtype dtype);
+kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v,
+                                const float* log_decay, const float* initial_state,
+                                const int32_t* cu_seqlens, int B, int T, int H, int dk, int dv,
+                                int num_seqs, kda_dtype dtype, void* o, float* final_state,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of kda_linear_chunk_fwd for L = sum <d_o, o> + sum <d_final_state,
+ * final_state>.  Nothing of the forward is needed but its inputs:
+ *
+ *     dq_t = d_k^{-1/2} S_t d_o_t,   G_t = lambda G_{t+1} + d_k^{-1/2} q_t d_o_t^T,
+ *     dk_t = G_t v_t,   dv_t = G_t^T k_t,   dS_0 = lambda G_1
+ *
+ * (G_T also holds d_final_state).  Arguments as kda_linear_chunk_fwd and
+ * kda_chunk_bwd; d_final_state NULL: zeros; d_initial_state NULL: not computed.
+ * Outputs must not overlap inputs.
+ */
+size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv,
+                                           int num_seqs, int varlen, kda_dtype dtype);
+kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v,
+                                const float* log_decay, const float* initial_state,
+                                const int32_t* cu_seqlens, const void* d_o,
+                                const float* d_final_state, int B, int T, int H, int dk, int dv,
+                                int num_seqs, kda_dtype dtype, void* dq, void* dk_out,
+                                void* dv_out, float* d_initial_state, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * One token of the same recurrence for B sequences, the state updated in place.
+ *  q, k [B, H, dk], v [B, H, dv] dtype; log_decay [H] fp32 or NULL;
+ *  state_inout [B, H, dk, dv] fp32; o [B, H, dv] dtype (must not alias the state)
+ */
+kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v,
+                                     const float* log_decay, float* state_inout, int B, int H,
+                                     int dk, int dv, kda_dtype dtype, void* o, void* stream);
+
+/*
+ * What queries and keys go through before any of the calls above: a norm over the
+ * channels of each head and, in the same pass, the position rotation.  Per token
+ * and head, for a row x of d channels:
+ *
+ *     n = x (sum x^2 / d + eps)^{-1/2} w      KDA_NORM_RMS
+ *     n = x (sum x^2     + eps)^{-1/2} w      KDA_NORM_L2
+ *     (y_a, y_b) = (n_a cos t - n_b sin t, n_b cos t + n_a sin t),   t = position * inv_freq[j]
+ *
+ * for pair j < rotary_dim / 2 of the first rotary_dim channels: (a, b) = (j, j +
+ * rotary_dim / 2), or (2j, 2j + 1) with `interleaved`; the other channels are only
+ * normed.  The angle is formed in fp64.
+ *
+ *  q           [B, T, Hq, d], k [B, T, Hk, d]: dtype, 16-byte aligned, the channels
+ *              of a head contiguous; q_strides / k_strides are the element strides
+ *              of batch, token and head (host arrays, multiples of 16 bytes), so a
+ *              slice of a joint projection is taken as it lies
+ *  q_weight, k_weight [d] fp32, or NULL for ones
+ *  inv_freq    [rotary_dim / 2] fp32 (NULL only with rotary_dim = 0)
+ *  positions   [B, T] int32, or NULL for 0 .. T-1 in every row of the batch
+ *  d           a multiple of 8 up to 256; rotary_dim a multiple of 16 up to d
+ *  eps         > 0: a row of zeros gives zeros
+ *  q_out       [B, T, Hq, d], k_out [B, T, Hk, d] dtype, contiguous, written; each
+ *              may be its (contiguous) input itself, and must not overlap it otherwise
+ */
+typedef enum { KDA_NORM_RMS = 0, KDA_NORM_L2 = 1 } kda_norm;
+kda_status kda_qk_norm_rope(const void* q, const void* k, const float* q_weight,
+                            const float* k_weight, const float* inv_freq,
+                            const int32_t* positions, int B, int T, int Hq, int Hk, int d,
+                            int rotary_dim, const int64_t* q_strides, const int64_t* k_strides,
+                            kda_dtype dtype, kda_norm norm, float eps, int interleaved,
+                            void* q_out, void* k_out, void* stream);
+
+/*
+ * Its gradients: dq, dk (contiguous, dtype) for the cotangents d_q_out, d_k_out
+ * (contiguous, dtype) of its outputs, and dq_weight, dk_weight [d] fp32 (each NULL
+ * if not wanted).  The sums over tokens run in a fixed order.  With either weight
+ * gradient the workspace needs kda_qk_norm_rope_bwd_workspace_size(d) bytes,
+ * 256-byte aligned; otherwise it may be NULL.  Other arguments as kda_qk_norm_rope
+ * (q, k: its inputs).  dq and dk must not overlap the inputs.
+ */
+size_t kda_qk_norm_rope_bwd_workspace_size(int d);
+kda_status kda_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out,
+                                const void* d_k_out, const float* q_weight,
+                                const float* k_weight, const float* inv_freq,
+                                const int32_t* positions, int B, int T, int Hq, int Hk, int d,
+                                int rotary_dim, const int64_t* q_strides,
+                                const int64_t* k_strides, kda_dtype dtype, kda_norm norm,
+                                float eps, int interleaved, void* dq, void* dk,
+                                float* dq_weight, float* dk_weight, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
  * Measurement hook for benchmarks.  When `events` is non-NULL, each later
  * kda_chunk_fwd on this host thread records the caller-created CUDA events
  * (cudaEvent_t passed as void*) on its stream at the stage boundaries:
