@@ -21,11 +21,12 @@
 //    it is returned in.
 //
 // One CTA per (segment, head, role), one per SM (TMEM: Z, P and two accumulators of
-// y, 512 columns).  Warp 9 loads tiles by TMA, warp 8 issues the MMAs, warps 0-3
-// weight P and write y, warps 4-7 weight c, convert and decay Z.  The chain from
-// chunk to chunk (Z -> operand -> Z^T a, update) and the rest overlap: b and c tiles
-// go through a ring of three buffers, so the next chunk's b is in flight while this
-// one is worked on, and a's buffer frees as soon as P and Z^T a are done.
+// y, 512 columns).  Warp 17 loads tiles by TMA, warp 16 issues the MMAs, warps 0-7
+// weight P and write y, warps 8-15 convert and decay Z and weight c.  The chain from
+// chunk to chunk (Z -> operand -> Z^T a, update) and the rest overlap: b and c have
+// two buffers each, so the next chunk's tiles are in flight while this one is worked
+// on; a's buffer frees as soon as P and Z^T a are done; y leaves through the buffer
+// of its own chunk's c (warp 18 sends it out by TMA).
 //
 // Every wait is bounded; one that gives up sets a flag that ends the CTA's other
 // waits, records KDA_ERR_TIMEOUT, and the CTA waits for its own copies and MMAs,
@@ -41,6 +42,7 @@ constexpr uint32_t kTile = 128 * 128;          // 128 tokens x 64 bf16 channels,
 
 struct LinTcParams {
     CUtensorMap map[4];                        // q, k, v, d_o
+    CUtensorMap ymap[kLinMaxRoles];            // each role's output
     LinArgs a;
 };
 
@@ -48,7 +50,7 @@ struct LinTcParams {
 __device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t parity, int* s_abort) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_for(bar, parity, 1000000u)) {
         if (*(volatile int*)s_abort) return false;
         if (clock64() - t0 > kWaitCycles) {
             *(volatile int*)s_abort = 1;
@@ -68,6 +70,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
+// x minus its bf16 part, exactly.
+__device__ __forceinline__ float2 rest_of(float2 x, uint32_t part) {
+    return fma2(unpack_bf16(part), make_float2(-1.f, -1.f), x);
+}
+
 template <int D>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar, int h, int tok) {
     mbar_arrive_expect_tx(bar, (D / 64) * kTile);
@@ -85,52 +106,62 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int D, int L, in
     }
 }
 
-// Tokens [64 half, 64 half + 64) of c, weighted, in `parts` bf16 parts of
-// D2 / 64 tiles of 64 rows each; 128 threads.  A row past L becomes zero.
-template <int D2>
-__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int half, int parts, int L,
+// ROWS tokens of c from row i0 on, weighted, in `parts` bf16 parts of D2 / 64 tiles
+// of ROWS rows each; 256 threads, eight channels of a row at a time.  A row past L
+// becomes zero.
+template <int D2, int ROWS>
+__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int i0, int parts, int L,
                                          const float* pw, float c_upd, bool rev, int t) {
-    constexpr uint32_t PART = (D2 / 64) * 8192;
+    constexpr uint32_t PART = (D2 / 64) * ROWS * 128;
     const int chunk = t & 7;
-#pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 16 + (t >> 3), i = 64 * half + r;
+#pragma unroll 1
+    for (int e0 = 0; e0 < ROWS * 8 * (D2 / 64); e0 += 256) {
+        const int e = e0 + t, r = (e >> 3) % ROWS, tile = (e >> 3) / ROWS, i = i0 + r;
+        if (tile >= D2 / 64) break;
         const bool on = i < L;
         const float w = on ? c_upd * pw[rev ? i + 1 : L - 1 - i] : 0.f;
+        uint4 raw = *reinterpret_cast<const uint4*>(ct + tile * kTile + sw128_offset(i, chunk * 16));
+        if (!on) raw = make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t p[3][4];
 #pragma unroll
-        for (int tile = 0; tile < D2 / 64; ++tile) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(ct + tile * kTile + sw128_offset(i, chunk * 16));
-            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-            uint32_t p[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = on ? w * bf16_lo(u[e]) : 0.f, y = on ? w * bf16_hi(u[e]) : 0.f;
-                p[0][e] = pack_bf16(x, y);
-                x -= bf16_lo(p[0][e]);
-                y -= bf16_hi(p[0][e]);
-                p[1][e] = pack_bf16(x, y);
-                x -= bf16_lo(p[1][e]);
-                y -= bf16_hi(p[1][e]);
-                p[2][e] = pack_bf16(x, y);
-            }
-            unsigned char* dst = out + tile * 8192 + sw128_offset(r, chunk * 16);
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-                if (q < parts) *reinterpret_cast<uint4*>(dst + q * PART) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
+        for (int k = 0; k < 4; ++k) {
+            float2 x = mul2(make_float2(w, w), unpack_bf16(u[k]));
+            p[0][k] = pack_bf16(x.x, x.y);
+            x = rest_of(x, p[0][k]);
+            p[1][k] = pack_bf16(x.x, x.y);
+            x = rest_of(x, p[1][k]);
+            p[2][k] = pack_bf16(x.x, x.y);
         }
+        unsigned char* dst = out + tile * (ROWS * 128) + sw128_offset(r, chunk * 16);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            if (q < parts) *reinterpret_cast<uint4*>(dst + q * PART) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
     }
 }
 
-// Z += b^T (weighted c) over 64 tokens.
-template <int D2>
-__device__ __forceinline__ void issue_update(uint32_t zacc, uint32_t bt, uint32_t cw, int half, int parts, bool first) {
+// A shared-memory descriptor and the one `bytes` further on (the address field
+// never carries: all tiles lie below 256 KB).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
+// D (+)= b^T (weighted c) over ROWS tokens from row i0 of b on: bd the descriptor of b
+// as MN-major A, cd that of the weighted c as MN-major B.  The smallest parts first:
+// the tensor core cuts each sum off, which costs least while the sum is small.
+template <int D2, int ROWS, int PARTS>
+__device__ __forceinline__ void issue_update_parts(uint32_t acc, uint64_t bd, uint64_t cd, int i0, bool first) {
     constexpr uint32_t idesc = instr_desc(kFmtBF16, 128, D2, true, true);
-    constexpr uint32_t PART = (D2 / 64) * 8192;
-    for (int q = 0; q < parts; ++q)
+    constexpr uint32_t PART = (D2 / 64) * ROWS * 128;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            mma_f16(zacc, smem_desc(bt + half * 8192 + ks * 2048, kTile, 1024, kLayoutSW128),
-                    smem_desc(cw + q * PART + ks * 2048, 8192, 1024, kLayoutSW128), idesc, !(first && q == 0 && ks == 0));
+    for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+        for (int ks = 0; ks < ROWS / 16; ++ks)
+            mma_f16(acc, desc_at(bd, i0 * 128 + ks * 2048), desc_at(cd, q * PART + ks * 2048), idesc,
+                    !(first && q == PARTS - 1 && ks == 0));
+}
+template <int D2, int ROWS>
+__device__ __forceinline__ void issue_update(uint32_t acc, uint64_t bd, uint64_t cd, int i0, int parts, bool first) {
+    if (parts == 3) issue_update_parts<D2, ROWS, 3>(acc, bd, cd, i0, first);
+    else issue_update_parts<D2, ROWS, 2>(acc, bd, cd, i0, first);
 }
 
 // A thread's row of Z between global memory (the user's layout or its transpose)
@@ -164,36 +195,48 @@ __device__ __forceinline__ void write_state(float* s, bool transposed, int i, in
 }
 
 // ------------------------------------------------------------- chunk kernel --
+constexpr int kLinStep = 32;        // tokens of one step of the update
+static_assert(C / kLinStep == 4, "the chunk kernel names its steps");
+
 template <int D1, int D2>
 struct LinSmem {
     static constexpr uint32_t AT = (D1 / 64) * kTile, CT = (D2 / 64) * kTile;
-    static constexpr uint32_t SLOT = AT > CT ? AT : CT;
     static constexpr uint32_t A = 0;
-    static constexpr uint32_t BC = A + AT;                       // ring of three b / c tiles
-    static constexpr uint32_t Z = BC + 3 * SLOT;                 // bf16 Z: D2 / 64 tiles of D1 rows
-    static constexpr uint32_t CW = Z + (D2 / 64) * D1 * 128;     // weighted c of 64 tokens, three parts
-    static constexpr uint32_t END = CW + 3 * (D2 / 64) * 8192;
+    static constexpr uint32_t B = A + AT;                        // b of two chunks
+    static constexpr uint32_t CC = B + 2 * AT;                   // c of two chunks; y leaves through its own chunk's
+    static constexpr uint32_t Z = CC + 2 * CT;                   // bf16 Z: D2 / 64 tiles of D1 rows
+    // Weighted c of one step, three parts.  Even steps have a place of their own, odd
+    // ones take Z's, which is read only by a Z, before the first of them.
+    static constexpr uint32_t CWB = 3 * (D2 / 64) * kLinStep * 128;
+    static constexpr uint32_t ZB = (D2 / 64) * D1 * 128 > CWB ? (D2 / 64) * D1 * 128 : CWB;
+    static constexpr uint32_t CW = Z + ZB;
+    static constexpr uint32_t END = CW + CWB;
     static_assert(END + 1024 + 1200 <= 232448, "shared memory");
 };
 
+constexpr int kLinThreads = 19 * 32;
+
 template <int D1, int D2>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kLinThreads, 1)
 linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 {
     using Sm = LinSmem<D1, D2>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t full_a, empty_a, full_bc[3], p_done, p_ready, y_done, y_free, cw_ready[2],
-        upd_done[2], z_ready, drained;
+    __shared__ __align__(8) uint64_t full_a, az_done, full_b[2], empty_b[2], full_c[2], empty_c[2], p_done, p_ready,
+        y_done, y_free, y_staged[2], cw_ready[2], cw_free[2], upd_done, z_ready, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ float pw[C + 1];
-    __shared__ __align__(16) float colw[32];
+    // weights of a 32 x 32 block of P, at [31 + row - column] for one on the diagonal (0 on the side that does not
+    // count) and [31 - column], times a factor of the row, for another
+    __shared__ float diag[64], edge[32];
 
     const LinArgs& args = prm.a;
     if (args.hdr->status != kStatusOk) return;
     int x = blockIdx.x;
-    const LinRole& role = args.role[x % args.roles];
+    const int ri = x % args.roles;
+    const LinRole& role = args.role[ri];
     x /= args.roles;
     const int H = args.H, h = x % H, sidx = x / H;
     if (sidx >= args.map.segments()) return;
@@ -203,21 +246,29 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t zsize = (size_t)D1 * D2, user = ((size_t)g.seq * H + h) * zsize;
     const int parts = role.s_out ? 3 : 2;
+    // in registers: the asm statements below make the compiler read memory again
+    const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
+    __nv_bfloat16* const yout = static_cast<__nv_bfloat16*>(role.y);
 
     if (tid == 0) {
         s_abort = 0;
         mbar_init(&full_a, 1);
-        mbar_init(&empty_a, 1);
-        for (int i = 0; i < 3; ++i) mbar_init(&full_bc[i], 1);
+        mbar_init(&az_done, 1);
         mbar_init(&p_done, 1);
-        mbar_init(&p_ready, 128);
+        mbar_init(&p_ready, 256);
         mbar_init(&y_done, 1);
-        mbar_init(&y_free, 128);
+        mbar_init(&y_free, 256);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&cw_ready[i], 128);
-            mbar_init(&upd_done[i], 1);
+            mbar_init(&full_b[i], 1);
+            mbar_init(&empty_b[i], 1);
+            mbar_init(&full_c[i], 1);
+            mbar_init(&empty_c[i], 1);
+            mbar_init(&y_staged[i], 256);
+            mbar_init(&cw_ready[i], 256);
+            mbar_init(&cw_free[i], 1);
         }
-        mbar_init(&z_ready, 128);
+        mbar_init(&upd_done, 1);
+        mbar_init(&z_ready, 256);
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
@@ -228,235 +279,292 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
     {
         const double l = lin_log_decay(args.log_decay, h);
         if (tid <= C) pw[tid] = lin_pow(l, tid);
-        if (tid < 32) colw[tid] = lin_pow(l, rev ? tid : 31 - tid);
+        else if (tid >= 160 && tid < 192) edge[tid - 160] = lin_pow(l, rev ? 191 - tid : tid - 160);
+        else if (tid >= 192 && tid < 255) {
+            const int n = rev ? 31 - (tid - 192) : tid - 192 - 31;
+            diag[tid - 192] = n >= 0 ? lin_pow(l, n) : 0.f;
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const uint32_t ZACC = tmem, PACC = tmem + 128, YZ = tmem + 256, YP = tmem + 384;
+    const uint32_t ZREG = tmem, UACC = tmem + 128, PACC = tmem + 256, YACC = tmem + 384;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const int row = (warp & 3) * 32 + lane;
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const int sub = (warp >> 2) & 1;            // the two warps of a group that share 32 TMEM lanes split the columns
     auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
+    // b and c of chunk n are use n / 2 of their buffer n % 2
+    auto buf_b = [&](int n) { return sm + Sm::B + (n & 1) * Sm::AT; };
+    auto buf_c = [&](int n) { return sm + Sm::CC + (n & 1) * Sm::CT; };
 
-    if (warp == 9) {                                    // ---- TMA loads
+    if (warp == 17) {                                   // ---- TMA loads
         if (lane == 0) {
-            int issued[3] = {0, 0, 0}, issued_a = 0;
-            bool ok = true;
-            for (int n = 0; ok && n < nch; ++n) {
-                const int tok = g.begin + chunk_of(n) * C;
-                int j = 2 * n;                          // b: the buffer of chunk n - 2's c, waited for with chunk n - 1's c
-                load_tile<D1>(sm + Sm::BC + (j % 3) * Sm::SLOT, &prm.map[role.b], &full_bc[j % 3], h, tok);
-                ++issued[j % 3];
-                if (n > 0) ok = lin_wait(&empty_a, (n - 1) & 1, &s_abort);
-                if (!ok) break;
+            int nb = 0, nc = 0, na = 0;
+            for (int n = 0; n < nch; ++n) {             // in the order in which the buffers become free
+                const int tok = g.begin + chunk_of(n) * C, i = n & 1;
+                const uint32_t before = ((n >> 1) - 1) & 1;
+                if (n > 1 && !lin_wait(&empty_b[i], before, &s_abort)) break;
+                load_tile<D1>(buf_b(n), &prm.map[role.b], &full_b[i], h, tok);
+                ++nb;
+                if (n > 1 && !lin_wait(&empty_c[i], before, &s_abort)) break;
+                load_tile<D2>(buf_c(n), &prm.map[role.c], &full_c[i], h, tok);
+                ++nc;
+                if (n > 0 && !lin_wait(&az_done, (n - 1) & 1, &s_abort)) break;
                 load_tile<D1>(sm + Sm::A, &prm.map[role.a], &full_a, h, tok);
-                ++issued_a;
-                if (n > 0) ok = lin_wait(&upd_done[1], (n - 1) & 1, &s_abort);
-                if (!ok) break;
-                j = 2 * n + 1;                          // c: the buffer of chunk n - 1's b
-                load_tile<D2>(sm + Sm::BC + (j % 3) * Sm::SLOT, &prm.map[role.c], &full_bc[j % 3], h, tok);
-                ++issued[j % 3];
+                ++na;
             }
             // every copy issued has landed before the CTA's memory goes away
-            if (issued_a) (void)mbar_wait_cycles(&full_a, (issued_a - 1) & 1, kWaitCycles);
-            for (int i = 0; i < 3; ++i)
-                if (issued[i]) (void)mbar_wait_cycles(&full_bc[i], (issued[i] - 1) & 1, kWaitCycles);
+            if (na) (void)mbar_wait_cycles(&full_a, (na - 1) & 1, kWaitCycles);
+            for (int n = max(nb - 2, 0); n < nb; ++n) (void)mbar_wait_cycles(&full_b[n & 1], (n >> 1) & 1, kWaitCycles);
+            for (int n = max(nc - 2, 0); n < nc; ++n) (void)mbar_wait_cycles(&full_c[n & 1], (n >> 1) & 1, kWaitCycles);
         }
-    } else if (warp == 8) {                             // ---- MMA issue
+    } else if (warp == 18) {                            // ---- y out, from c's buffer
         if (lane == 0) {
-            const uint32_t at = smem_u32(sm + Sm::A), zt = smem_u32(sm + Sm::Z), cw = smem_u32(sm + Sm::CW);
             for (int n = 0; n < nch; ++n) {
-                const uint32_t ph = n & 1, prev = (n - 1) & 1;
-                const int jb = 2 * n, jc = 2 * n + 1;
-                const uint32_t bt = smem_u32(sm + Sm::BC + (jb % 3) * Sm::SLOT);
-                const uint32_t ct = smem_u32(sm + Sm::BC + (jc % 3) * Sm::SLOT);
-                // P = a b^T, over the previous chunk's weighted P once y has been formed from it
-                if (!lin_wait(&full_a, ph, &s_abort) || !lin_wait(&full_bc[jb % 3], (jb / 3) & 1, &s_abort)) break;
-                if (n > 0 && !lin_wait(&y_done, prev, &s_abort)) break;
-                tc_fence_after();
-                constexpr uint32_t id_p = instr_desc(kFmtBF16, 128, 128);
+                if (!lin_wait(&y_staged[n & 1], (n >> 1) & 1, &s_abort)) break;
+                const int ch = chunk_of(n);
+                if (g.len - ch * C >= C) {              // a short chunk's rows have been written one by one
+#pragma unroll
+                    for (int t = 0; t < D2 / 64; ++t)
+                        tma_store_3d(&prm.ymap[ri], buf_c(n) + t * kTile, 64 * t, h, g.begin + ch * C);
+                    bulk_store_commit();
+                    bulk_store_wait_read();
+                }
+                mbar_arrive(&empty_c[n & 1]);
+            }
+            bulk_store_wait_all();
+        }
+    } else if (warp == 16) {                            // ---- MMA issue
+        // the whole warp goes through the loop together; one lane issues
+        // descriptors: K-major a, b; MN-major b (the update's A), Z, c, weighted c in its two places
+        const uint64_t a_k = smem_desc(smem_u32(sm + Sm::A), 16, 1024, kLayoutSW128);
+        const uint64_t z_mn = smem_desc(smem_u32(sm + Sm::Z), D1 * 128, 1024, kLayoutSW128);
+        const uint64_t w_mn0 = smem_desc(smem_u32(sm + Sm::CW), kLinStep * 128, 1024, kLayoutSW128);
+        const uint64_t w_mn1 = smem_desc(smem_u32(sm + Sm::Z), kLinStep * 128, 1024, kLayoutSW128);
+        const uint64_t b_k0 = smem_desc(smem_u32(sm + Sm::B), 16, 1024, kLayoutSW128);
+        const uint64_t b_mn0 = smem_desc(smem_u32(sm + Sm::B), kTile, 1024, kLayoutSW128);
+        const uint64_t c_mn0 = smem_desc(smem_u32(sm + Sm::CC), kTile, 1024, kLayoutSW128);
+        constexpr uint32_t id_p = instr_desc(kFmtBF16, 128, 128);
+        constexpr uint32_t id_y = instr_desc(kFmtBF16, 128, D2, false, true);
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t ph = n & 1, prev = (n - 1) & 1;
+            const uint64_t b_k = desc_at(b_k0, (n & 1) * Sm::AT), b_mn = desc_at(b_mn0, (n & 1) * Sm::AT);
+            const uint64_t c_mn = desc_at(c_mn0, (n & 1) * Sm::CT);
+            // P = a b^T, over the previous chunk's weighted P once y has been formed from it
+            if (!lin_wait_warp(&full_a, ph, &s_abort) || !lin_wait_warp(&full_b[n & 1], (n >> 1) & 1, &s_abort)) break;
+            if (n > 0 && !lin_wait_warp(&y_done, prev, &s_abort)) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D1 / 16; ++k) {
                     const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-                    mma_f16(PACC, smem_desc(at + off, 16, 1024, kLayoutSW128), smem_desc(bt + off, 16, 1024, kLayoutSW128),
-                            id_p, k != 0);
+                    mma_f16(PACC, desc_at(a_k, off), desc_at(b_k, off), id_p, k != 0);
                 }
                 mma_commit(&p_done);
-                // a Z
-                if (!lin_wait(&z_ready, ph, &s_abort)) break;
-                if (n > 0 && !lin_wait(&y_free, prev, &s_abort)) break;
-                tc_fence_after();
-                constexpr uint32_t id_y = instr_desc(kFmtBF16, 128, D2, false, true);
+            }
+            // y = a Z
+            if (!lin_wait_warp(&z_ready, ph, &s_abort) || (n > 0 && !lin_wait_warp(&y_free, prev, &s_abort))) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D1 / 16; ++k)
-                    mma_f16(YZ, smem_desc(at + (k >> 2) * kTile + (k & 3) * 32, 16, 1024, kLayoutSW128),
-                            smem_desc(zt + k * 2048, D1 * 128, 1024, kLayoutSW128), id_y, k != 0);
-                mma_commit(&empty_a);
-                // first half of the update
-                if (!lin_wait(&cw_ready[0], ph, &s_abort)) break;
-                tc_fence_after();
-                issue_update<D2>(ZACC, bt, cw, 0, parts, false);
-                mma_commit(&upd_done[0]);
-                // P c, both parts of P (16 columns of 32 each)
-                if (!lin_wait(&p_ready, ph, &s_abort)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        mma_f16_ts(YP, PACC + (k >> 1) * 32 + q * 16 + (k & 1) * 8,
-                                   smem_desc(ct + k * 2048, kTile, 1024, kLayoutSW128), id_y, (k | q) != 0);
-                mma_commit(&y_done);
-                // second half of the update
-                if (!lin_wait(&cw_ready[1], ph, &s_abort)) break;
-                tc_fence_after();
-                issue_update<D2>(ZACC, bt, cw, 1, parts, false);
-                mma_commit(&upd_done[1]);
+                    mma_f16(YACC, desc_at(a_k, (k >> 2) * kTile + (k & 3) * 32), desc_at(z_mn, k * 2048), id_y, k != 0);
+                mma_commit(&az_done);
             }
-            mma_commit(&drained);
-            (void)mbar_wait_cycles(&drained, 0, kWaitCycles);
+            // U = b^T (weighted c), as its operands come
+            bool ok = true;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                ok = lin_wait_warp(&cw_ready[i & 1], (i >> 1) & 1, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_update<D2, kLinStep>(UACC, b_mn, i & 1 ? w_mn1 : w_mn0, kLinStep * i, parts, i == 0);
+                    mma_commit(&cw_free[i & 1]);
+                    if (i == 3) {
+                        mma_commit(&upd_done);
+                        mma_commit(&empty_b[n & 1]);
+                    }
+                }
+            }
+            // y += P c last: Z's next operand is formed meanwhile
+            if (!ok || !lin_wait_warp(&p_ready, ph, &s_abort)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)             // both parts of P (8 columns of 16 each)
+#pragma unroll
+                    for (int q = 1; q >= 0; --q)
+                        mma_f16_ts(YACC, PACC + k * 16 + q * 8, desc_at(c_mn, k * 2048), id_y, true);
+                mma_commit(&y_done);
+            }
         }
-    } else if (warp < 4) {                              // ---- P and y
+        if (elect_one()) mma_commit(&drained);
+        (void)mbar_wait_cycles(&drained, 0, kWaitCycles);
+    } else if (warp < 8) {                              // ---- P, then y
         for (int n = 0; n < nch; ++n) {
-            const uint32_t ph = n & 1;
-            const int ch = chunk_of(n), L = min(C, g.len - ch * C);
-            if (!lin_wait_warp(&p_done, ph, &s_abort)) break;
+            const int ch = chunk_of(n), L = min(C, g.len - ch * C), tok = g.begin + ch * C;
+            if (!lin_wait_warp(&p_done, n & 1, &s_abort)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
+            for (int b = sub; b < 4; b += 2) {
                 const uint32_t at = PACC + lane_base + 32 * b;
-                float v[32];
                 uint32_t pk[32];
-                const bool some = rev ? b >= warp : b <= warp;      // this warp's rows see this block of columns
-                if (some) {
+                if (rev ? b >= quad : b <= quad) {      // these rows see this block of columns
+                    float v[32];
                     tmem_ld32_sync(at, v);
-                    if (b == warp) {
+                    if (L < C) {                        // columns past L hold other tokens' products
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int lag = rev ? j - lane : lane - j;
-                            v[j] = (lag >= 0 && 32 * b + j < L) ? pw[max(lag, 0)] * v[j] : 0.f;
-                        }
-                    } else {
-                        // |r - i| = (distance to the block's near edge) + (distance within it): both factors <= 1
-                        const float f = pw[rev ? 32 * b - row : row - (32 * b + 31)];
-                        const int left = L - 32 * b;
-#pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4) {
-                            const float4 w = *reinterpret_cast<const float4*>(&colw[4 * j4]);
-                            v[4 * j4] = 4 * j4 < left ? f * w.x * v[4 * j4] : 0.f;
-                            v[4 * j4 + 1] = 4 * j4 + 1 < left ? f * w.y * v[4 * j4 + 1] : 0.f;
-                            v[4 * j4 + 2] = 4 * j4 + 2 < left ? f * w.z * v[4 * j4 + 2] : 0.f;
-                            v[4 * j4 + 3] = 4 * j4 + 3 < left ? f * w.w * v[4 * j4 + 3] : 0.f;
-                        }
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * b + j >= L) v[j] = 0.f;
                     }
+                    // off the diagonal |r - i| = (distance to the block's near edge) + (distance within it): both factors <= 1
+                    const bool on = b == quad;
+                    const float f = c_intra * (on ? 1.f : pw[rev ? 32 * b - row : row - (32 * b + 31)]);
+                    const float* w = on ? diag + 31 + lane : edge + 31;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                        pk[16 + j] = pack_bf16(v[2 * j] - bf16_lo(pk[j]), v[2 * j + 1] - bf16_hi(pk[j]));
+                        const float2 x = mul2(make_float2(v[2 * j], v[2 * j + 1]), mul2(make_float2(f, f), make_float2(w[-2 * j], w[-2 * j - 1])));
+                        const uint32_t hi = pack_bf16(x.x, x.y);
+                        const float2 y = rest_of(x, hi);
+                        pk[(j >> 3) * 16 + (j & 7)] = hi;           // per 16 columns: 8 of the first part, 8 of the second
+                        pk[(j >> 3) * 16 + 8 + (j & 7)] = pack_bf16(y.x, y.y);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) pk[j] = 0;
                 }
-                float out[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(pk[j]);
-                tmem_st32_sync(at, out);
+                tmem_st32(at, pk);
             }
+            // y's rows of a Z get their weight, P c goes on top
+            if (!lin_wait_warp(&az_done, n & 1, &s_abort)) break;
+            tc_fence_after();
+            const float wz = c_inter * pw[row < L ? (rev ? L - 1 - row : row + 1) : 0];
+#pragma unroll 1
+            for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
+                float v[32];
+                uint32_t d[32];
+                tmem_ld32_sync(YACC + lane_base + j0, v);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 x = mul2(make_float2(wz, wz), make_float2(v[j], v[j + 1]));
+                    d[j] = __float_as_uint(x.x);
+                    d[j + 1] = __float_as_uint(x.y);
+                }
+                tmem_st32(YACC + lane_base + j0, d);
+            }
+            tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_ready);
-            if (!lin_wait_warp(&y_done, ph, &s_abort)) break;
+
+            if (!lin_wait_warp(&y_done, n & 1, &s_abort)) break;
             tc_fence_after();
-            const float wz = role.c_inter * pw[row < L ? (rev ? L - 1 - row : row + 1) : 0], wp = role.c_intra;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(role.y) +
-                                 ((size_t)(g.begin + ch * C + row) * H + h) * D2;
 #pragma unroll 1
-            for (int j0 = 0; j0 < D2; j0 += 32) {
-                float vz[32], vp[32];
-                tmem_ld32_sync(YZ + lane_base + j0, vz);
-                tmem_ld32_sync(YP + lane_base + j0, vp);
-                if (row < L) {
+            for (int j0 = 32 * sub; j0 < D2; j0 += (j0 & 16) ? 48 : 16) {
+                float v[16];
+                uint32_t y[8];
+                tmem_ld16_sync(YACC + lane_base + j0, v);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = pack_bf16(fmaf(wz, vz[j + 2 * e], wp * vp[j + 2 * e]),
-                                             fmaf(wz, vz[j + 2 * e + 1], wp * vp[j + 2 * e + 1]));
-                        *reinterpret_cast<uint4*>(dst + j0 + j) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                for (int e = 0; e < 8; ++e) y[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                if (L == C) {       // through c's place, which nothing reads any more, and out by TMA as whole rows
+                    unsigned char* dst = buf_c(n) + (j0 >> 6) * kTile;
+                    *reinterpret_cast<uint4*>(dst + sw128_offset(row, (j0 & 63) * 2)) = lo;
+                    *reinterpret_cast<uint4*>(dst + sw128_offset(row, (j0 & 63) * 2 + 16)) = hi;
+                } else if (row < L) {   // a short chunk: a tile would reach into the next sequence
+                    uint4* dst = reinterpret_cast<uint4*>(yout + ((size_t)(tok + row) * H + h) * D2 + j0);
+                    dst[0] = lo;
+                    dst[1] = hi;
                 }
             }
             tc_fence_before();
             mbar_arrive(&y_free);
+            fence_proxy_async_smem();
+            mbar_arrive(&y_staged[n & 1]);
         }
-    } else {                                            // ---- weighted c and Z
-        const int t = tid - 128;
+    } else {                                            // ---- Z, then the weighted c
+        const int t = tid - 256;
         bool ok = true;
-        if (row < D1 || D1 == 128) {
+        const bool mine = D1 == 128 || quad < 2;        // warps with rows of Z
+        if (mine) {
             const float* from = g.count > 1 ? role.seg + ((size_t)sidx * H + h) * zsize
                                             : (role.s_in ? role.s_in + user : nullptr);
 #pragma unroll 1
-            for (int j0 = 0; j0 < D2; j0 += 32) {
+            for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
                 read_state<D1, D2>(from, g.count == 1 && role.transposed, row, j0, v);
-                tmem_st32_sync(ZACC + lane_base + j0, v);
+                tmem_st32_sync(ZREG + lane_base + j0, v);
             }
         }
-        for (int n = 0; n < nch; ++n) {
-            const uint32_t ph = n & 1;
-            const int L = min(C, g.len - chunk_of(n) * C), jb = 2 * n, jc = 2 * n + 1;
-            unsigned char* bt = sm + Sm::BC + (jb % 3) * Sm::SLOT;
-            unsigned char* ct = sm + Sm::BC + (jc % 3) * Sm::SLOT;
-            if (n > 0) {
-                ok = lin_wait_warp(&upd_done[1], (n - 1) & 1, &s_abort);
-                if (!ok) break;
-                tc_fence_after();
-            }
-            if (row < D1 || D1 == 128) {                // Z -> bf16 operand, decayed in place
-                const float gam = pw[L];
-#pragma unroll 1
-                for (int j0 = 0; j0 < D2; j0 += 32) {
-                    float v[32];
-                    tmem_ld32_sync(ZACC + lane_base + j0, v);
-                    unsigned char* zt = sm + Sm::Z + (j0 >> 6) * (D1 * 128);
-#pragma unroll
-                    for (int j8 = 0; j8 < 4; ++j8)
-                        *reinterpret_cast<uint4*>(zt + sw128_offset(row, ((j0 & 63) + 8 * j8) * 2)) =
-                            make_uint4(pack_bf16(v[8 * j8], v[8 * j8 + 1]), pack_bf16(v[8 * j8 + 2], v[8 * j8 + 3]),
-                                       pack_bf16(v[8 * j8 + 4], v[8 * j8 + 5]), pack_bf16(v[8 * j8 + 6], v[8 * j8 + 7]));
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= gam;
-                    tmem_st32_sync(ZACC + lane_base + j0, v);
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            mbar_arrive(&z_ready);
-            ok = lin_wait_warp(&full_bc[jb % 3], (jb / 3) & 1, &s_abort) &&
-                 lin_wait_warp(&full_bc[jc % 3], (jc / 3) & 1, &s_abort);
+        for (int n = 0; ok && n < nch; ++n) {
+            const int L = min(C, g.len - chunk_of(n) * C), len_before = n > 0 ? min(C, g.len - chunk_of(n - 1) * C) : 0;
+            ok = lin_wait_warp(&full_b[n & 1], (n >> 1) & 1, &s_abort) && lin_wait_warp(&full_c[n & 1], (n >> 1) & 1, &s_abort);
             if (!ok) break;
             if (L < C) {        // P's MMA may still read b: its columns past L are dropped when P is weighted
-                clear_rows(bt, D1, L, 0, C, t, 128);
-                clear_rows(ct, D2, L, 0, C, t, 128);
+                clear_rows(buf_b(n), D1, L, 0, C, t, 256);
+                clear_rows(buf_c(n), D2, L, 0, C, t, 256);
+                fence_proxy_async_smem();
             }
-            weight_c<D2>(ct, sm + Sm::CW, 0, parts, L, pw, role.c_upd, rev, t);
-            fence_proxy_async_smem();
-            mbar_arrive(&cw_ready[0]);
-            ok = lin_wait_warp(&upd_done[0], ph, &s_abort);
-            if (!ok) break;
-            weight_c<D2>(ct, sm + Sm::CW, 1, parts, L, pw, role.c_upd, rev, t);
-            fence_proxy_async_smem();
-            mbar_arrive(&cw_ready[1]);
-        }
-        if (ok && nch > 0) ok = lin_wait_warp(&upd_done[1], (nch - 1) & 1, &s_abort);
-        if (ok && role.s_out && g.index == (rev ? 0 : g.count - 1) && (row < D1 || D1 == 128)) {
-            tc_fence_after();
 #pragma unroll 1
-            for (int j0 = 0; j0 < D2; j0 += 32) {
+            for (int i = 0; i < 4; ++i) {
+                if (i == 1) {       // step 0 is ahead of Z, while the previous chunk's update runs
+                    if (n > 0) ok = lin_wait_warp(&upd_done, (n - 1) & 1, &s_abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (mine) {                         // Z <- lambda^L Z + U of the previous chunk; its bf16 operand
+                        const float gam = n > 0 ? pw[len_before] : 1.f;
+#pragma unroll 1
+                        for (int j0 = 32 * sub; j0 < D2; j0 += (j0 & 16) ? 48 : 16) {
+                            float v[16], u[16];
+                            tmem_ld16x2_sync(ZREG + lane_base + j0, UACC + lane_base + j0, v, u);
+                            if (n > 0) {
+                                uint32_t d[16];
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) {
+                                    const float2 x = fma2(make_float2(gam, gam), make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
+                                    v[j] = x.x; v[j + 1] = x.y;
+                                    d[j] = __float_as_uint(x.x);
+                                    d[j + 1] = __float_as_uint(x.y);
+                                }
+                                tmem_st16(ZREG + lane_base + j0, d);
+                            }
+                            unsigned char* zt = sm + Sm::Z + (j0 >> 6) * (D1 * 128);
+#pragma unroll
+                            for (int j8 = 0; j8 < 2; ++j8)
+                                *reinterpret_cast<uint4*>(zt + sw128_offset(row, (j0 & 63) * 2 + 16 * j8)) =
+                                    make_uint4(pack_bf16(v[8 * j8], v[8 * j8 + 1]), pack_bf16(v[8 * j8 + 2], v[8 * j8 + 3]),
+                                               pack_bf16(v[8 * j8 + 4], v[8 * j8 + 5]), pack_bf16(v[8 * j8 + 6], v[8 * j8 + 7]));
+                        }
+                        tmem_wait_st();
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&z_ready);
+                }
+                // the step's place is free: of the step two before, or (odd, first) of Z's operand
+                if (i == 1) ok = lin_wait_warp(&az_done, n & 1, &s_abort);
+                else if (n > 0 || i > 1) ok = lin_wait_warp(&cw_free[i & 1], i > 1 ? 0 : 1, &s_abort);
+                if (!ok) break;
+                weight_c<D2, kLinStep>(buf_c(n), sm + (i & 1 ? Sm::Z : Sm::CW), kLinStep * i, parts, L, pw, c_upd, rev, t);
+                fence_proxy_async_smem();
+                mbar_arrive(&cw_ready[i & 1]);
+            }
+        }
+        if (ok && nch > 0) ok = lin_wait_warp(&upd_done, (nch - 1) & 1, &s_abort);
+        if (ok && mine && role.s_out && g.index == (rev ? 0 : g.count - 1)) {
+            tc_fence_after();
+            const float gam = nch > 0 ? pw[min(C, g.len - chunk_of(nch - 1) * C)] : 1.f;
+#pragma unroll 1
+            for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
-                tmem_ld32_sync(ZACC + lane_base + j0, v);
+                tmem_ld32_sync(ZREG + lane_base + j0, v);
+                if (nch > 0) {
+                    float u[32];
+                    tmem_ld32_sync(UACC + lane_base + j0, u);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = fmaf(gam, v[j], u[j]);
+                }
                 write_state<D1, D2>(role.s_out + user, role.transposed, row, j0, v);
             }
         }
@@ -469,9 +577,10 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 
 // ----------------------------------------------------------- segment's sum --
 // Z of one segment from zero: sum_i lambda^{tokens from i to the segment's end}
-// b_i c_i^T.  The weights count to the segment's end, so nothing is rescaled and
-// the MMAs only accumulate; warps 0-3 weight the first 64 tokens of each chunk,
-// warps 4-7 the other 64, each into a buffer of its own.
+// b_i c_i^T.  The weights count to the segment's end, so nothing is rescaled.  Each
+// chunk's sum is formed in TMEM (two of them, in turn) and added in registers, 64
+// elements a thread: the tensor core's cut-off sums would pile up over a long
+// segment.  Half a chunk of c is weighted while the other half is multiplied.
 template <int D1, int D2>
 struct LinSumSmem {
     static constexpr uint32_t BT = (D1 / 64) * kTile, CT = (D2 / 64) * kTile;
@@ -489,7 +598,7 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     using Sm = LinSumSmem<D1, D2>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t full[2], empty[2], cw_ready[2], upd_done[2], drained;
+    __shared__ __align__(8) uint64_t full[2], empty[2], cw_ready[2], cw_free[2], upd_done, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ float pw[C + 1];
@@ -507,6 +616,7 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     const int nch = (g.len + C - 1) / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = role.s_out ? 3 : 2;
+    const float c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
 
     if (tid == 0) {
@@ -514,14 +624,15 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], 2);
             mbar_init(&empty[i], 1);
-            mbar_init(&cw_ready[i], 128);
-            mbar_init(&upd_done[i], 1);
+            mbar_init(&cw_ready[i], 256);
+            mbar_init(&cw_free[i], 1);
         }
+        mbar_init(&upd_done, 1);
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(&s_tmem, 128);
+        tmem_alloc(&s_tmem, 256);
         tmem_relinquish();
     }
     if (tid <= C) pw[tid] = lin_pow(l, tid);
@@ -531,7 +642,7 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     const uint32_t tmem = s_tmem;
     auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
 
-    if (warp == 9) {
+    if (warp == 9) {                                    // ---- TMA loads
         if (lane == 0) {
             int n = 0;
             for (; n < nch; ++n) {
@@ -545,58 +656,86 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
                 if (count > 0) (void)mbar_wait_cycles(&full[i], (count - 1) & 1, kWaitCycles);
             }
         }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            bool ok = true;
-            for (int n = 0; ok && n < nch; ++n) {
-                const uint32_t bt = smem_u32(sm + (n & 1) * Sm::STAGE);
-                ok = lin_wait(&full[n & 1], (n >> 1) & 1, &s_abort);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = ok && lin_wait(&cw_ready[half], n & 1, &s_abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_update<D2>(tmem, bt, smem_u32(sm + Sm::CW + half * Sm::CWH), half, parts, n == 0 && half == 0);
-                    mma_commit(&upd_done[half]);
-                }
-                if (ok) mma_commit(&empty[n & 1]);
-            }
-            mma_commit(&drained);
-            (void)mbar_wait_cycles(&drained, 0, kWaitCycles);
-        }
-    } else {
-        const int half = warp >> 2, t = tid & 127;
+    } else if (warp == 8) {                             // ---- MMA issue
+        const uint64_t b_mn0 = smem_desc(smem_u32(sm), kTile, 1024, kLayoutSW128);
+        const uint64_t w_mn0 = smem_desc(smem_u32(sm + Sm::CW), 64 * 128, 1024, kLayoutSW128);
         bool ok = true;
-        int after = 0;                                  // tokens of this segment after the chunk, in its direction
-        for (int n = 0; n < nch; ++n) {
-            const int ch = chunk_of(n), L = min(C, g.len - ch * C);
-            after = rev ? ch * C : g.len - ch * C - L;
-            unsigned char* bt = sm + (n & 1) * Sm::STAGE;
-            ok = lin_wait_warp(&full[n & 1], (n >> 1) & 1, &s_abort) &&
-                 (n == 0 || lin_wait_warp(&upd_done[half], (n - 1) & 1, &s_abort));
-            if (!ok) break;
-            if (L < C) clear_rows(bt, D1, L, 64 * half, 64 * half + 64, t, 128);
-            weight_c<D2>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, half, parts, L, pw, role.c_upd * lin_pow(l, after), rev, t);
-            fence_proxy_async_smem();
-            mbar_arrive(&cw_ready[half]);
-        }
-        ok = ok && lin_wait_warp(&upd_done[1], (nch - 1) & 1, &s_abort);
-        const int row = (warp & 3) * 32 + lane;
-        if (ok && half == 0 && (row < D1 || D1 == 128)) {
-            tc_fence_after();
-            float* to = role.seg + ((size_t)sidx * H + h) * D1 * D2;
+        for (int n = 0; ok && n < nch; ++n) {
+            const uint64_t b_mn = desc_at(b_mn0, (n & 1) * Sm::STAGE);
+            ok = lin_wait_warp(&full[n & 1], (n >> 1) & 1, &s_abort);
 #pragma unroll 1
-            for (int j0 = 0; j0 < D2; j0 += 32) {
-                float v[32];
-                tmem_ld32_sync(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j0, v);
-                write_state<D1, D2>(to, false, row, j0, v);
+            for (int half = 0; ok && half < 2; ++half) {
+                ok = lin_wait_warp(&cw_ready[half], n & 1, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_update<D2, 64>(tmem + 128 * (n & 1), b_mn, desc_at(w_mn0, half * Sm::CWH), 64 * half, parts, half == 0);
+                    mma_commit(&cw_free[half]);
+                    if (half == 1) {
+                        mma_commit(&upd_done);
+                        mma_commit(&empty[n & 1]);
+                    }
+                }
             }
+        }
+        if (elect_one()) mma_commit(&drained);
+        (void)mbar_wait_cycles(&drained, 0, kWaitCycles);
+    } else {                                            // ---- weighted c, the sum
+        const int quad = warp & 3, sub = warp >> 2, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
+        constexpr int COLS = D2 / 2;                    // columns COLS sub .. of this thread's row
+        float z[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) z[j] = 0.f;
+        auto add = [&](int n) {                         // Z += chunk n's sum
+            if (!lin_wait_warp(&upd_done, n & 1, &s_abort)) return false;
+            tc_fence_after();
+            if (D1 == 128 || quad < 2) {
+#pragma unroll
+                for (int j0 = 0; j0 < COLS; j0 += 32) {
+                    float v[32];
+                    tmem_ld32_sync(tmem + 128 * (n & 1) + lane_base + COLS * sub + j0, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j0 + j] += v[j];
+                }
+            }
+            tc_fence_before();
+            return true;
+        };
+        bool ok = true;
+        for (int n = 0; ok && n < nch; ++n) {
+            const int ch = chunk_of(n), L = min(C, g.len - ch * C);
+            const int after = rev ? ch * C : g.len - ch * C - L;    // tokens of the segment still to come
+            unsigned char* bt = sm + (n & 1) * Sm::STAGE;
+            const float cw = c_upd * lin_pow(l, after);
+            ok = lin_wait_warp(&full[n & 1], (n >> 1) & 1, &s_abort);
+            if (!ok) break;
+            if (L < C) {
+                clear_rows(bt, D1, L, 0, C, tid, 256);
+                fence_proxy_async_smem();
+            }
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                // the last chunk's sum before this chunk's second half, without which the barrier cannot go on
+                if (n > 0) ok = lin_wait_warp(&cw_free[half], (n - 1) & 1, &s_abort) && (half == 0 || add(n - 1));
+                if (!ok) break;
+                weight_c<D2, 64>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, 64 * half, parts, L, pw, cw, rev, tid);
+                fence_proxy_async_smem();
+                mbar_arrive(&cw_ready[half]);
+            }
+        }
+        if (ok) ok = add(nch - 1);
+        if (ok && (D1 == 128 || quad < 2)) {
+            float* to = role.seg + ((size_t)sidx * H + h) * D1 * D2 + (size_t)row * D2 + COLS * sub;
+#pragma unroll
+            for (int j = 0; j < COLS; j += 4)
+                *reinterpret_cast<float4*>(to + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && s_abort) flag_error(args.hdr, kStatusTimeout);
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
 template <int D1, int D2>
@@ -606,7 +745,7 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const int smem = (int)(states_only ? LinSumSmem<D1, D2>::END : LinSmem<D1, D2>::END) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), 320, smem, a.stream>>>(p);
+    kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? 320 : kLinThreads, smem, a.stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -618,16 +757,20 @@ cudaError_t launch_linear_tc(const LinArgs& a, bool states_only) {
     p.a = a;
     auto fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
-    for (int i = 0; i < 4; ++i) {
-        if (!a.x[i] || a.tokens == 0) continue;
-        // [tokens, H, d] in boxes of 64 channels x 1 head x 128 tokens
-        const cuuint64_t dims[3] = {(cuuint64_t)a.dim[i], (cuuint64_t)a.H, (cuuint64_t)a.tokens};
-        const cuuint64_t strides[2] = {(cuuint64_t)a.dim[i] * 2, (cuuint64_t)a.H * a.dim[i] * 2};
+    // [tokens, H, d] in boxes of 64 channels x 1 head x 128 tokens
+    auto encode = [&](CUtensorMap* m, const void* base, int d) {
+        const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)a.H, (cuuint64_t)a.tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.H * d * 2};
         const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)C}, estr[3] = {1u, 1u, 1u};
-        if (fn(&p.map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.x[i]), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (a.tokens > 0) {
+        for (int i = 0; i < 4; ++i)
+            if (a.x[i] && !encode(&p.map[i], a.x[i], a.dim[i])) return cudaErrorInvalidValue;
+        for (int i = 0; !states_only && i < a.roles; ++i)
+            if (!encode(&p.ymap[i], a.role[i].y, a.dim[a.role[i].c])) return cudaErrorInvalidValue;
     }
     const int d1 = a.dim[a.role[0].a], d2 = a.dim[a.role[0].c];   // the same for all roles of one launch
     if (d1 == 128 && d2 == 128) return launch_tc_t<128, 128>(p, states_only);
