@@ -106,23 +106,25 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int D, int L, in
     }
 }
 
-// ROWS tokens of c from row i0 on, weighted, in `parts` bf16 parts of D2 / 64 tiles
-// of ROWS rows each; 256 threads, eight channels of a row at a time.  A row past L
-// becomes zero.
+// 32 tokens of c from row i0 on, weighted, in `parts` bf16 parts of D2 / 64 tiles of
+// ROWS rows each, into rows r0.. of those; 256 threads, eight channels of each tile a
+// thread.  A row past L becomes zero.
 template <int D2, int ROWS>
-__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int i0, int parts, int L,
+__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int i0, int r0, int parts, int L,
                                          const float* pw, float c_upd, bool rev, int t) {
     constexpr uint32_t PART = (D2 / 64) * ROWS * 128;
-    const int chunk = t & 7;
-#pragma unroll 1
-    for (int e0 = 0; e0 < ROWS * 8 * (D2 / 64); e0 += 256) {
-        const int e = e0 + t, r = (e >> 3) % ROWS, tile = (e >> 3) / ROWS, i = i0 + r;
-        if (tile >= D2 / 64) break;
-        const bool on = i < L;
-        const float w = on ? c_upd * pw[rev ? i + 1 : L - 1 - i] : 0.f;
-        uint4 raw = *reinterpret_cast<const uint4*>(ct + tile * kTile + sw128_offset(i, chunk * 16));
-        if (!on) raw = make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    const int i = i0 + (t >> 3);
+    const uint32_t src = sw128_offset(i, (t & 7) * 16);
+    const bool on = i < L;
+    uint4 raw[D2 / 64];
+#pragma unroll
+    for (int tile = 0; tile < D2 / 64; ++tile) raw[tile] = *reinterpret_cast<const uint4*>(ct + tile * kTile + src);
+    const float w = on ? c_upd * pw[rev ? i + 1 : L - 1 - i] : 0.f;
+    out += sw128_offset(r0 + (t >> 3), (t & 7) * 16);
+#pragma unroll
+    for (int tile = 0; tile < D2 / 64; ++tile) {
+        if (!on) raw[tile] = make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {raw[tile].x, raw[tile].y, raw[tile].z, raw[tile].w};
         uint32_t p[3][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -133,10 +135,10 @@ __device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char*
             x = rest_of(x, p[1][k]);
             p[2][k] = pack_bf16(x.x, x.y);
         }
-        unsigned char* dst = out + tile * (ROWS * 128) + sw128_offset(r, chunk * 16);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            if (q < parts) *reinterpret_cast<uint4*>(dst + q * PART) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
+            if (q < parts)
+                *reinterpret_cast<uint4*>(out + tile * (ROWS * 128) + q * PART) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
     }
 }
 
@@ -205,8 +207,8 @@ struct LinSmem {
     static constexpr uint32_t B = A + AT;                        // b of two chunks
     static constexpr uint32_t CC = B + 2 * AT;                   // c of two chunks; y leaves through its own chunk's
     static constexpr uint32_t Z = CC + 2 * CT;                   // bf16 Z: D2 / 64 tiles of D1 rows
-    // Weighted c of one step, three parts.  Even steps have a place of their own, odd
-    // ones take Z's, which is read only by a Z, before the first of them.
+    // Weighted c of one step, three parts: steps 0 and 1 have a place of their own, 2 and
+    // 3 take that of Z's operand, which nothing reads after a Z.
     static constexpr uint32_t CWB = 3 * (D2 / 64) * kLinStep * 128;
     static constexpr uint32_t ZB = (D2 / 64) * D1 * 128 > CWB ? (D2 / 64) * D1 * 128 : CWB;
     static constexpr uint32_t CW = Z + ZB;
@@ -363,8 +365,19 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                 }
                 mma_commit(&p_done);
             }
-            // y = a Z
-            if (!lin_wait_warp(&z_ready, ph, &s_abort) || (n > 0 && !lin_wait_warp(&y_free, prev, &s_abort))) break;
+            // U = b^T (weighted c) in four steps, as their operands come; between them y = a Z and,
+            // on top of its weighted rows, y += P c
+            auto update = [&](int i) {
+                const bool ok = lin_wait_warp(&cw_ready[i >> 1], i & 1, &s_abort);
+                tc_fence_after();
+                if (ok && elect_one()) {
+                    issue_update<D2, kLinStep>(UACC, b_mn, i < 2 ? w_mn0 : w_mn1, kLinStep * i, parts, i == 0);
+                    mma_commit(&cw_free[i >> 1]);
+                }
+                return ok;
+            };
+            if (!lin_wait_warp(&z_ready, ph, &s_abort) || !update(0)) break;
+            if (n > 0 && !lin_wait_warp(&y_free, prev, &s_abort)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -372,24 +385,7 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                     mma_f16(YACC, desc_at(a_k, (k >> 2) * kTile + (k & 3) * 32), desc_at(z_mn, k * 2048), id_y, k != 0);
                 mma_commit(&az_done);
             }
-            // U = b^T (weighted c), as its operands come
-            bool ok = true;
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                ok = lin_wait_warp(&cw_ready[i & 1], (i >> 1) & 1, &s_abort);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    issue_update<D2, kLinStep>(UACC, b_mn, i & 1 ? w_mn1 : w_mn0, kLinStep * i, parts, i == 0);
-                    mma_commit(&cw_free[i & 1]);
-                    if (i == 3) {
-                        mma_commit(&upd_done);
-                        mma_commit(&empty_b[n & 1]);
-                    }
-                }
-            }
-            // y += P c last: Z's next operand is formed meanwhile
-            if (!ok || !lin_wait_warp(&p_ready, ph, &s_abort)) break;
+            if (!update(1) || !update(2) || !lin_wait_warp(&p_ready, ph, &s_abort)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -398,6 +394,11 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                     for (int q = 1; q >= 0; --q)
                         mma_f16_ts(YACC, PACC + k * 16 + q * 8, desc_at(c_mn, k * 2048), id_y, true);
                 mma_commit(&y_done);
+            }
+            if (!update(3)) break;
+            if (elect_one()) {
+                mma_commit(&upd_done);
+                mma_commit(&empty_b[n & 1]);
             }
         }
         if (elect_one()) mma_commit(&drained);
@@ -458,24 +459,32 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
             tc_fence_before();
             mbar_arrive(&p_ready);
 
-            if (!lin_wait_warp(&y_done, n & 1, &s_abort)) break;
+            // the update's last step, while P c runs
+            if (!lin_wait_warp(&full_c[n & 1], (n >> 1) & 1, &s_abort) || !lin_wait_warp(&cw_free[1], 0, &s_abort)) break;
+            weight_c<D2, kLinStep>(buf_c(n), sm + Sm::Z, 3 * kLinStep, 0, parts, L, pw, c_upd, rev, tid);
+            fence_proxy_async_smem();
+            mbar_arrive(&cw_ready[1]);
+
+            // y, through c's place: P c has been formed, and all eight warps have weighted their c
+            if (!lin_wait_warp(&y_done, n & 1, &s_abort) || !lin_wait_warp(&cw_ready[1], 1, &s_abort)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int j0 = 32 * sub; j0 < D2; j0 += (j0 & 16) ? 48 : 16) {
-                float v[16];
-                uint32_t y[8];
-                tmem_ld16_sync(YACC + lane_base + j0, v);
+            for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
+                float v[32];
+                tmem_ld32_sync(YACC + lane_base + j0, v);
+                uint4 y[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                if (L == C) {       // through c's place, which nothing reads any more, and out by TMA as whole rows
-                    unsigned char* dst = buf_c(n) + (j0 >> 6) * kTile;
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(row, (j0 & 63) * 2)) = lo;
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(row, (j0 & 63) * 2 + 16)) = hi;
+                for (int e = 0; e < 4; ++e)
+                    y[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                                      pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+                if (L == C) {       // out by TMA as whole rows
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(buf_c(n) + (j0 >> 6) * kTile + sw128_offset(row, 64 * sub + 16 * e)) = y[e];
                 } else if (row < L) {   // a short chunk: a tile would reach into the next sequence
                     uint4* dst = reinterpret_cast<uint4*>(yout + ((size_t)(tok + row) * H + h) * D2 + j0);
-                    dst[0] = lo;
-                    dst[1] = hi;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[e] = y[e];
                 }
             }
             tc_fence_before();
@@ -507,7 +516,7 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                 fence_proxy_async_smem();
             }
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 3; ++i) {
                 if (i == 1) {       // step 0 is ahead of Z, while the previous chunk's update runs
                     if (n > 0) ok = lin_wait_warp(&upd_done, (n - 1) & 1, &s_abort);
                     if (!ok) break;
@@ -515,24 +524,23 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                     if (mine) {                         // Z <- lambda^L Z + U of the previous chunk; its bf16 operand
                         const float gam = n > 0 ? pw[len_before] : 1.f;
 #pragma unroll 1
-                        for (int j0 = 32 * sub; j0 < D2; j0 += (j0 & 16) ? 48 : 16) {
-                            float v[16], u[16];
-                            tmem_ld16x2_sync(ZREG + lane_base + j0, UACC + lane_base + j0, v, u);
+                        for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
+                            float v[32], u[32];
+                            tmem_ld32x2_sync(ZREG + lane_base + j0, UACC + lane_base + j0, v, u);
                             if (n > 0) {
-                                uint32_t d[16];
+                                uint32_t d[32];
 #pragma unroll
-                                for (int j = 0; j < 16; j += 2) {
+                                for (int j = 0; j < 32; j += 2) {
                                     const float2 x = fma2(make_float2(gam, gam), make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
                                     v[j] = x.x; v[j + 1] = x.y;
                                     d[j] = __float_as_uint(x.x);
                                     d[j + 1] = __float_as_uint(x.y);
                                 }
-                                tmem_st16(ZREG + lane_base + j0, d);
+                                tmem_st32(ZREG + lane_base + j0, d);
                             }
-                            unsigned char* zt = sm + Sm::Z + (j0 >> 6) * (D1 * 128);
 #pragma unroll
-                            for (int j8 = 0; j8 < 2; ++j8)
-                                *reinterpret_cast<uint4*>(zt + sw128_offset(row, (j0 & 63) * 2 + 16 * j8)) =
+                            for (int j8 = 0; j8 < 4; ++j8)
+                                *reinterpret_cast<uint4*>(sm + Sm::Z + (j0 >> 6) * (D1 * 128) + sw128_offset(row, 64 * sub + 16 * j8)) =
                                     make_uint4(pack_bf16(v[8 * j8], v[8 * j8 + 1]), pack_bf16(v[8 * j8 + 2], v[8 * j8 + 3]),
                                                pack_bf16(v[8 * j8 + 4], v[8 * j8 + 5]), pack_bf16(v[8 * j8 + 6], v[8 * j8 + 7]));
                         }
@@ -542,13 +550,13 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
                     tc_fence_before();
                     mbar_arrive(&z_ready);
                 }
-                // the step's place is free: of the step two before, or (odd, first) of Z's operand
-                if (i == 1) ok = lin_wait_warp(&az_done, n & 1, &s_abort);
-                else if (n > 0 || i > 1) ok = lin_wait_warp(&cw_free[i & 1], i > 1 ? 0 : 1, &s_abort);
+                // the step's place is free: of the step before, or (step 2) of Z's operand
+                if (i == 2) ok = lin_wait_warp(&az_done, n & 1, &s_abort);
+                else if (n > 0 || i == 1) ok = lin_wait_warp(&cw_free[0], i == 0, &s_abort);
                 if (!ok) break;
-                weight_c<D2, kLinStep>(buf_c(n), sm + (i & 1 ? Sm::Z : Sm::CW), kLinStep * i, parts, L, pw, c_upd, rev, t);
+                weight_c<D2, kLinStep>(buf_c(n), sm + (i < 2 ? Sm::CW : Sm::Z), kLinStep * i, 0, parts, L, pw, c_upd, rev, t);
                 fence_proxy_async_smem();
-                mbar_arrive(&cw_ready[i & 1]);
+                mbar_arrive(&cw_ready[i >> 1]);
             }
         }
         if (ok && nch > 0) ok = lin_wait_warp(&upd_done, (nch - 1) & 1, &s_abort);
@@ -719,7 +727,9 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
                 // the last chunk's sum before this chunk's second half, without which the barrier cannot go on
                 if (n > 0) ok = lin_wait_warp(&cw_free[half], (n - 1) & 1, &s_abort) && (half == 0 || add(n - 1));
                 if (!ok) break;
-                weight_c<D2, 64>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, 64 * half, parts, L, pw, cw, rev, tid);
+#pragma unroll
+                for (int r = 0; r < 64; r += 32)
+                    weight_c<D2, 64>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, 64 * half + r, r, parts, L, pw, cw, rev, tid);
                 fence_proxy_async_smem();
                 mbar_arrive(&cw_ready[half]);
             }
