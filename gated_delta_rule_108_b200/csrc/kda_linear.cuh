@@ -103,8 +103,22 @@ struct LinArgs {
     int roles;
     LinRole role[kLinMaxRoles];
     WsHeader* hdr;
+    bool reset;                   // the launch starts the call: block 0 clears the status
     cudaStream_t stream;
 };
+
+// What every kernel of a call begins with: true where the call goes on.  The
+// segment table's kernel has left the status of a packed batch; otherwise the first
+// launch clears it (block 0 is among the first to run, and another block records an
+// error only after a wait of a second).
+__device__ __forceinline__ bool lin_begin(const LinArgs& a) {
+    if (a.map.cu) return a.hdr->status == kStatusOk;
+    if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) {
+        a.hdr->status = kStatusOk;
+        a.hdr->runtime_err = 0;
+    }
+    return true;
+}
 
 // Powers of a head's decay: e^(l n), from a 64-bit exponent; l is kept finite so
 // that l n is 0 at n = 0 also for l = -inf (a state forgotten at every token).

@@ -125,8 +125,11 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     LinArgs all = a;
     for (int i = 0; i < all.roles; ++i)
         all.role[i].seg = p.split ? reinterpret_cast<float*>(ws + p.seg_off + p.seg_bytes * i) : nullptr;
-    cudaError_t e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
+    cudaError_t e = cudaSuccess;
+    if (all.map.cu) e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
+    else if (p.max_segments == 0) e = cudaMemsetAsync(all.hdr, 0, sizeof(WsHeader), all.stream);
     if (p.max_segments == 0) return e;
+    all.reset = true;
     auto pass = [&](bool states_only) {
         bool done[kLinMaxRoles] = {};
         for (int i = 0; i < all.roles && e == cudaSuccess; ++i) {
@@ -139,6 +142,7 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
                     done[j] = true;
                 }
             e = a.bf16 ? launch_linear_tc(one, states_only) : launch_linear_simt(one, states_only);
+            all.reset = false;
         }
     };
     if (p.split && e == cudaSuccess) {

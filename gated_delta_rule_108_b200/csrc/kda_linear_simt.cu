@@ -13,9 +13,12 @@
 // m_i = i + 1 last to first (a cotangent decays when it leaves its token, a state
 // before it enters).
 #include "kda_linear.cuh"
+#include "ptx.cuh"
 
 namespace kda {
 namespace {
+
+using namespace ptx;
 
 // ------------------------------------------------------------- segments --
 // Packed sequences: checks cu, orders the sequences longest first (up to 4096 of
@@ -30,10 +33,6 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
     __shared__ int warp_sums[32];
     __shared__ int s_carry, s_bad, s_max;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (cu == nullptr) {
-        if (tid == 0) { hdr->status = kStatusOk; hdr->runtime_err = 0; }
-        return;
-    }
     if (tid == 0) { s_carry = 0; s_max = 0; s_bad = (cu[0] != 0 || cu[N] != T) ? 1 : 0; }
     __syncthreads();
     for (int s = tid; s < N; s += 1024) {
@@ -108,7 +107,7 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
 __global__ void __launch_bounds__(256)
 linear_scan_kernel(const __grid_constant__ LinArgs a)
 {
-    if (a.hdr->status != kStatusOk) return;
+    if (!lin_begin(a)) return;
     const LinRole& role = a.role[blockIdx.z];
     const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
     int seq, first, count;
@@ -149,23 +148,30 @@ template <int D1>
 struct LinSimtSmem {
     static constexpr int LDA = D1 + 4;           // rows 16 bytes apart in the banks: float4 reads of 8 rows do not clash
     static constexpr int LDC = kSimtCols, LDP = kSimtChunk + 4;
-    float a[kSimtChunk][LDA], b[kSimtChunk][LDA];
-    float c[kSimtChunk][LDC], p[kSimtChunk][LDP], z[D1][LDC];
+    struct Tile { float a[kSimtChunk][LDA], b[kSimtChunk][LDA], c[kSimtChunk][LDC]; } tile[2];
+    float p[kSimtChunk][LDP], z[D1][LDC];
     float pw[kSimtChunk + 1];
 };
 
+// y += p c, a row's four columns.
+__device__ __forceinline__ void axpy(float2 (&y)[2], float p, const float4& c) {
+    y[0] = fma2(make_float2(p, p), make_float2(c.x, c.y), y[0]);
+    y[1] = fma2(make_float2(p, p), make_float2(c.z, c.w), y[1]);
+}
+
 // One CTA per (segment, head, 64 columns of D2); 256 threads.  A thread owns 4 x 4
 // of P and of y (rows ty + 16 n) and D1 / 16 x 4 of Z, which stays in registers
-// with a copy in shared memory for the read.  Bound by FMA issue: 64 FMAs per 8
-// 16-byte shared-memory reads.
-template <typename T, int D1, int D2>
+// with a copy in shared memory for the read.  Bound by FMA issue (two at a time,
+// 32 instructions per 8 16-byte shared-memory reads); the next chunk's tiles arrive
+// by cp.async meanwhile, rows past a segment's end as zeros.
+template <int D1, int D2>
 __global__ void __launch_bounds__(256)
 linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
 {
     using Sm = LinSimtSmem<D1>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
-    if (args.hdr->status != kStatusOk) return;
+    if (!lin_begin(args)) return;
     constexpr int SL = D2 / kSimtCols, ZR = D1 / 16;
     int x = blockIdx.x;
     const int slice = x % SL;
@@ -180,65 +186,80 @@ linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
     if (states_only && last) return;
     const int j0 = slice * kSimtCols;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
     for (int n = tid; n <= kSimtChunk; n += 256) sm.pw[n] = lin_pow(l, n);
 
     const size_t zsize = (size_t)D1 * D2;
     const size_t user = ((size_t)g.seq * H + h) * zsize;
     float* seg = role.seg ? role.seg + ((size_t)sidx * H + h) * zsize : nullptr;
-    float4 z[ZR];
+    const float* pa = static_cast<const float*>(args.x[role.a]);
+    const float* pb = static_cast<const float*>(args.x[role.b]);
+    const float* pc = static_cast<const float*>(args.x[role.c]);
+    float* py = static_cast<float*>(role.y);
+    const int nch = (g.len + kSimtChunk - 1) / kSimtChunk;
+    auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
+    auto fetch = [&](int n) {                    // chunk n's tiles on their way
+        if (n < nch) {
+            typename Sm::Tile& t = sm.tile[n & 1];
+            const int off = chunk_of(n) * kSimtChunk, L = min(kSimtChunk, g.len - off), tok0 = g.begin + off;
+            for (int e = tid; e < kSimtChunk * (D1 / 4); e += 256) {
+                const int r = e / (D1 / 4), i = 4 * (e % (D1 / 4));
+                const size_t at = ((size_t)(tok0 + min(r, L - 1)) * H + h) * D1 + i;
+                cp_async16(&t.b[r][i], pb + at, r < L ? 16 : 0);
+                if (!states_only) cp_async16(&t.a[r][i], pa + at, r < L ? 16 : 0);
+            }
+            for (int e = tid; e < kSimtChunk * (kSimtCols / 4); e += 256) {
+                const int r = e / (kSimtCols / 4), j = 4 * (e % (kSimtCols / 4));
+                cp_async16(&t.c[r][j], pc + ((size_t)(tok0 + min(r, L - 1)) * H + h) * D2 + j0 + j, r < L ? 16 : 0);
+            }
+        }
+        cp_async_commit();
+    };
+    fetch(0);
+
+    float2 z[ZR][2];
     const float* from = states_only ? nullptr : (g.count > 1 ? seg : (role.s_in ? role.s_in + user : nullptr));
     const bool tr_in = g.count == 1 && role.transposed;
 #pragma unroll
     for (int n = 0; n < ZR; ++n) {
         const int i = ty * ZR + n, j = j0 + 4 * tx;
-        z[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (from)
-            z[n] = tr_in ? make_float4(from[(size_t)j * D1 + i], from[(size_t)(j + 1) * D1 + i],
-                                       from[(size_t)(j + 2) * D1 + i], from[(size_t)(j + 3) * D1 + i])
-                         : *reinterpret_cast<const float4*>(from + (size_t)i * D2 + j);
+            v = tr_in ? make_float4(from[(size_t)j * D1 + i], from[(size_t)(j + 1) * D1 + i],
+                                    from[(size_t)(j + 2) * D1 + i], from[(size_t)(j + 3) * D1 + i])
+                      : *reinterpret_cast<const float4*>(from + (size_t)i * D2 + j);
+        z[n][0] = make_float2(v.x, v.y);
+        z[n][1] = make_float2(v.z, v.w);
     }
-    const T* pa = static_cast<const T*>(args.x[role.a]);
-    const T* pb = static_cast<const T*>(args.x[role.b]);
-    const T* pc = static_cast<const T*>(args.x[role.c]);
-    T* py = static_cast<T*>(role.y);
-    const int nch = (g.len + kSimtChunk - 1) / kSimtChunk;
     for (int n = 0; n < nch; ++n) {
-        const int ch = rev ? nch - 1 - n : n;
+        const int ch = chunk_of(n);
         const int tok0 = g.begin + ch * kSimtChunk, L = min(kSimtChunk, g.len - ch * kSimtChunk);
-        __syncthreads();                         // the previous chunk's reads are done
-        for (int e = tid; e < kSimtChunk * D1; e += 256) {
-            const int r = e / D1, i = e - r * D1;
-            const size_t at = ((size_t)(tok0 + r) * H + h) * D1 + i;
-            sm.b[r][i] = r < L ? to_f32(pb[at]) : 0.f;
-            if (!states_only) sm.a[r][i] = r < L ? to_f32(pa[at]) : 0.f;
-        }
-        for (int e = tid; e < kSimtChunk * kSimtCols; e += 256) {
-            const int r = e / kSimtCols, j = e - r * kSimtCols;
-            sm.c[r][j] = r < L ? to_f32(pc[((size_t)(tok0 + r) * H + h) * D2 + j0 + j]) : 0.f;
-        }
+        typename Sm::Tile& t = sm.tile[n & 1];
+        cp_async_wait<0>();
         if (!states_only) {
 #pragma unroll
-            for (int i = 0; i < ZR; ++i) *reinterpret_cast<float4*>(&sm.z[ty * ZR + i][4 * tx]) = z[i];
+            for (int i = 0; i < ZR; ++i)
+                *reinterpret_cast<float4*>(&sm.z[ty * ZR + i][4 * tx]) = make_float4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
         }
-        __syncthreads();
+        __syncthreads();                         // chunk n has landed; chunk n - 1 has been read by all
+        fetch(n + 1);
         if (!states_only) {
-            float acc[4][4] = {};
+            float2 acc[4][4] = {};
+#pragma unroll 4
             for (int i = 0; i < D1; i += 4) {
                 float4 av[4], bv[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    av[m] = *reinterpret_cast<const float4*>(&sm.a[ty + 16 * m][i]);
-                    bv[m] = *reinterpret_cast<const float4*>(&sm.b[tx + 16 * m][i]);
+                    av[m] = *reinterpret_cast<const float4*>(&t.a[ty + 16 * m][i]);
+                    bv[m] = *reinterpret_cast<const float4*>(&t.b[tx + 16 * m][i]);
                 }
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        acc[m][k] = fmaf(av[m].x, bv[k].x, acc[m][k]);
-                        acc[m][k] = fmaf(av[m].y, bv[k].y, acc[m][k]);
-                        acc[m][k] = fmaf(av[m].z, bv[k].z, acc[m][k]);
-                        acc[m][k] = fmaf(av[m].w, bv[k].w, acc[m][k]);
+                        acc[m][k] = fma2(make_float2(av[m].x, av[m].y), make_float2(bv[k].x, bv[k].y), acc[m][k]);
+                        acc[m][k] = fma2(make_float2(av[m].z, av[m].w), make_float2(bv[k].z, bv[k].w), acc[m][k]);
                     }
             }
 #pragma unroll
@@ -246,76 +267,64 @@ linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int lag = rev ? (tx + 16 * k) - (ty + 16 * m) : (ty + 16 * m) - (tx + 16 * k);
-                    sm.p[ty + 16 * m][tx + 16 * k] = lag >= 0 ? sm.pw[lag] * acc[m][k] : 0.f;
+                    sm.p[ty + 16 * m][tx + 16 * k] = lag >= 0 ? c_intra * sm.pw[lag] * (acc[m][k].x + acc[m][k].y) : 0.f;
                 }
             __syncthreads();
-            float4 in[4], out[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                in[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-                out[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            auto axpy = [](float4& y, float p, const float4& c) {
-                y.x = fmaf(p, c.x, y.x); y.y = fmaf(p, c.y, y.y);
-                y.z = fmaf(p, c.z, y.z); y.w = fmaf(p, c.w, y.w);
-            };
-            for (int i = 0; i < kSimtChunk; i += 4) {
-                float4 c0 = *reinterpret_cast<const float4*>(&sm.c[i][4 * tx]);
-                float4 c1 = *reinterpret_cast<const float4*>(&sm.c[i + 1][4 * tx]);
-                float4 c2 = *reinterpret_cast<const float4*>(&sm.c[i + 2][4 * tx]);
-                float4 c3 = *reinterpret_cast<const float4*>(&sm.c[i + 3][4 * tx]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float4 p = *reinterpret_cast<const float4*>(&sm.p[ty + 16 * m][i]);
-                    axpy(in[m], p.x, c0); axpy(in[m], p.y, c1); axpy(in[m], p.z, c2); axpy(in[m], p.w, c3);
-                }
-            }
+            float2 out[4][2] = {};
+#pragma unroll 4
             for (int i = 0; i < D1; i += 4) {
-                float4 c0 = *reinterpret_cast<const float4*>(&sm.z[i][4 * tx]);
-                float4 c1 = *reinterpret_cast<const float4*>(&sm.z[i + 1][4 * tx]);
-                float4 c2 = *reinterpret_cast<const float4*>(&sm.z[i + 2][4 * tx]);
-                float4 c3 = *reinterpret_cast<const float4*>(&sm.z[i + 3][4 * tx]);
+                const float4 c0 = *reinterpret_cast<const float4*>(&sm.z[i][4 * tx]);
+                const float4 c1 = *reinterpret_cast<const float4*>(&sm.z[i + 1][4 * tx]);
+                const float4 c2 = *reinterpret_cast<const float4*>(&sm.z[i + 2][4 * tx]);
+                const float4 c3 = *reinterpret_cast<const float4*>(&sm.z[i + 3][4 * tx]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const float4 p = *reinterpret_cast<const float4*>(&sm.a[ty + 16 * m][i]);
+                    const float4 p = *reinterpret_cast<const float4*>(&t.a[ty + 16 * m][i]);
                     axpy(out[m], p.x, c0); axpy(out[m], p.y, c1); axpy(out[m], p.z, c2); axpy(out[m], p.w, c3);
                 }
             }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const int r = ty + 16 * m;
-                if (r < L) {
-                    const float w = role.c_inter * sm.pw[rev ? L - 1 - r : r + 1];
-                    T* dst = py + ((size_t)(tok0 + r) * H + h) * D2 + j0 + 4 * tx;
-                    dst[0] = from_f32<T>(fmaf(w, out[m].x, role.c_intra * in[m].x));
-                    dst[1] = from_f32<T>(fmaf(w, out[m].y, role.c_intra * in[m].y));
-                    dst[2] = from_f32<T>(fmaf(w, out[m].z, role.c_intra * in[m].z));
-                    dst[3] = from_f32<T>(fmaf(w, out[m].w, role.c_intra * in[m].w));
-                }
+                const float w = c_inter * sm.pw[r < L ? (rev ? L - 1 - r : r + 1) : 0];
+                out[m][0] = mul2(make_float2(w, w), out[m][0]);
+                out[m][1] = mul2(make_float2(w, w), out[m][1]);
             }
-            __syncthreads();                     // c is weighted in place next
-        }
-        for (int e = tid; e < kSimtChunk * kSimtCols; e += 256) {
-            const int r = e / kSimtCols;
-            if (r < L) sm.c[r][e - r * kSimtCols] *= role.c_upd * sm.pw[rev ? r + 1 : L - 1 - r];
-        }
-        __syncthreads();
-        const float w = sm.pw[L];
-#pragma unroll
-        for (int i = 0; i < ZR; ++i) { z[i].x *= w; z[i].y *= w; z[i].z *= w; z[i].w *= w; }
-        for (int r = 0; r < kSimtChunk; ++r) {
-            const float4 c = *reinterpret_cast<const float4*>(&sm.c[r][4 * tx]);
-#pragma unroll
-            for (int i = 0; i < ZR; i += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(&sm.b[r][ty * ZR + i]);
-                const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 4
+            for (int i = 0; i < kSimtChunk; i += 4) {
+                const float4 c0 = *reinterpret_cast<const float4*>(&t.c[i][4 * tx]);
+                const float4 c1 = *reinterpret_cast<const float4*>(&t.c[i + 1][4 * tx]);
+                const float4 c2 = *reinterpret_cast<const float4*>(&t.c[i + 2][4 * tx]);
+                const float4 c3 = *reinterpret_cast<const float4*>(&t.c[i + 3][4 * tx]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    z[i + m].x = fmaf(bb[m], c.x, z[i + m].x);
-                    z[i + m].y = fmaf(bb[m], c.y, z[i + m].y);
-                    z[i + m].z = fmaf(bb[m], c.z, z[i + m].z);
-                    z[i + m].w = fmaf(bb[m], c.w, z[i + m].w);
+                    const float4 p = *reinterpret_cast<const float4*>(&sm.p[ty + 16 * m][i]);
+                    axpy(out[m], p.x, c0); axpy(out[m], p.y, c1); axpy(out[m], p.z, c2); axpy(out[m], p.w, c3);
                 }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int r = ty + 16 * m;
+                if (r < L)
+                    *reinterpret_cast<float4*>(py + ((size_t)(tok0 + r) * H + h) * D2 + j0 + 4 * tx) =
+                        make_float4(out[m][0].x, out[m][0].y, out[m][1].x, out[m][1].y);
+            }
+        }
+        const float w = sm.pw[L];
+#pragma unroll
+        for (int i = 0; i < ZR; ++i) {
+            z[i][0] = mul2(make_float2(w, w), z[i][0]);
+            z[i][1] = mul2(make_float2(w, w), z[i][1]);
+        }
+#pragma unroll 4
+        for (int r = 0; r < kSimtChunk; ++r) {
+            const float m = r < L ? c_upd * sm.pw[rev ? r + 1 : L - 1 - r] : 0.f;
+            float4 c = *reinterpret_cast<const float4*>(&t.c[r][4 * tx]);
+            c.x *= m; c.y *= m; c.z *= m; c.w *= m;
+#pragma unroll
+            for (int i = 0; i < ZR; i += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(&t.b[r][ty * ZR + i]);
+                axpy(z[i], b.x, c); axpy(z[i + 1], b.y, c); axpy(z[i + 2], b.z, c); axpy(z[i + 3], b.w, c);
             }
         }
     }
@@ -326,19 +335,19 @@ linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
     for (int n = 0; n < ZR; ++n) {
         const int i = ty * ZR + n, j = j0 + 4 * tx;
         if (tr_out) {
-            to[(size_t)j * D1 + i] = z[n].x;
-            to[(size_t)(j + 1) * D1 + i] = z[n].y;
-            to[(size_t)(j + 2) * D1 + i] = z[n].z;
-            to[(size_t)(j + 3) * D1 + i] = z[n].w;
+            to[(size_t)j * D1 + i] = z[n][0].x;
+            to[(size_t)(j + 1) * D1 + i] = z[n][0].y;
+            to[(size_t)(j + 2) * D1 + i] = z[n][1].x;
+            to[(size_t)(j + 3) * D1 + i] = z[n][1].y;
         } else {
-            *reinterpret_cast<float4*>(to + (size_t)i * D2 + j) = z[n];
+            *reinterpret_cast<float4*>(to + (size_t)i * D2 + j) = make_float4(z[n][0].x, z[n][0].y, z[n][1].x, z[n][1].y);
         }
     }
 }
 
-template <typename T, int D1, int D2>
+template <int D1, int D2>
 cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
-    auto kern = linear_simt_kernel<T, D1, D2>;
+    auto kern = linear_simt_kernel<D1, D2>;
     const int smem = (int)sizeof(LinSimtSmem<D1>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -350,7 +359,7 @@ cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
 }  // namespace
 
 cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens) {
-    linear_prep_kernel<<<1, a.map.cu ? 1024 : 32, 0, a.stream>>>(a.hdr, tab, a.map.cu, a.map.N, a.map.T, seg_tok,
+    linear_prep_kernel<<<1, 1024, 0, a.stream>>>(a.hdr, tab, a.map.cu, a.map.N, a.map.T, seg_tok,
                                                                  balance_tokens);
     return cudaGetLastError();
 }
@@ -364,10 +373,10 @@ cudaError_t launch_linear_scan(const LinArgs& a) {
 // All roles of one launch have the same (D1, D2): those of its first role's inputs.
 cudaError_t launch_linear_simt(const LinArgs& a, bool states_only) {
     const int d1 = a.dim[a.role[0].a], d2 = a.dim[a.role[0].c];
-    if (d1 == 128 && d2 == 128) return launch_simt_t<float, 128, 128>(a, states_only);
-    if (d1 == 128 && d2 == 64) return launch_simt_t<float, 128, 64>(a, states_only);
-    if (d1 == 64 && d2 == 128) return launch_simt_t<float, 64, 128>(a, states_only);
-    if (d1 == 64 && d2 == 64) return launch_simt_t<float, 64, 64>(a, states_only);
+    if (d1 == 128 && d2 == 128) return launch_simt_t<128, 128>(a, states_only);
+    if (d1 == 128 && d2 == 64) return launch_simt_t<128, 64>(a, states_only);
+    if (d1 == 64 && d2 == 128) return launch_simt_t<64, 128>(a, states_only);
+    if (d1 == 64 && d2 == 64) return launch_simt_t<64, 64>(a, states_only);
     return cudaErrorInvalidValue;
 }
 

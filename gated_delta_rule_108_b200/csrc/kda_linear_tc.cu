@@ -63,32 +63,6 @@ __device__ __forceinline__ bool lin_wait_warp(uint64_t* bar, uint32_t parity, in
     return __all_sync(0xffffffffu, lin_wait(bar, parity, s_abort));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-
-// Two fp32 operations at once.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_bf16(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
-// x minus its bf16 part, exactly.
-__device__ __forceinline__ float2 rest_of(float2 x, uint32_t part) {
-    return fma2(unpack_bf16(part), make_float2(-1.f, -1.f), x);
-}
-
 template <int D>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar, int h, int tok) {
     mbar_arrive_expect_tx(bar, (D / 64) * kTile);
@@ -235,7 +209,7 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
     __shared__ float diag[64], edge[32];
 
     const LinArgs& args = prm.a;
-    if (args.hdr->status != kStatusOk) return;
+    if (!lin_begin(args)) return;
     int x = blockIdx.x;
     const int ri = x % args.roles;
     const LinRole& role = args.role[ri];
@@ -612,7 +586,7 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     __shared__ float pw[C + 1];
 
     const LinArgs& args = prm.a;
-    if (args.hdr->status != kStatusOk) return;
+    if (!lin_begin(args)) return;
     int x = blockIdx.x;
     const LinRole& role = args.role[x % args.roles];
     x /= args.roles;

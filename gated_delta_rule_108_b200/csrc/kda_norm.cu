@@ -12,13 +12,15 @@
 //   dx = r h - m r^3 <h, x> x,   dw = sum over tokens and heads of g r x
 //
 // Both read each row once and write it once: HBM bandwidth bounds them at size,
-// launch latency for a handful of tokens.  A lane holds eight channels of a row, so
-// LPR = d / 8 lanes (rounded up to 8, 16 or 32) share a row and a warp takes
-// 32 / LPR rows at a time; the sums are butterflies over those lanes.  A warp works
-// on the heads of one token (or a slab of them when there are few tokens), so its
-// angles are computed once per token and kept in registers.  An angle is
-// pos * freq in fp64, reduced to a turn before it is rounded to fp32: positions of
-// 10^6 keep every bit of the angle that fp32 can hold.
+// launch latency for a handful of tokens.  A lane holds eight channels of a row, in
+// two groups of four chosen so that the two channels of a pair lie in one lane
+// (4 l.. and 4 l + rotary_dim / 2.. where halves are paired), so LPR = d / 8 lanes
+// (rounded up to 8, 16 or 32) share a row, a warp takes 32 / LPR rows at a time and
+// the row's sums are the only exchange.  A warp works on the heads of one token (or
+// a slab of them when there are few tokens): angle and weight of each channel are
+// one pair of factors, formed once per token for queries and once for keys.  An
+// angle is pos * freq in fp64, reduced to a turn before it is rounded to fp32:
+// positions of 10^6 keep every bit of the angle that fp32 can hold.
 #include "kda_common.cuh"
 #include "kda_launch.h"
 #include "../../include/kda.h"
@@ -30,7 +32,6 @@ namespace {
 
 constexpr int kWarps = 8;              // per CTA
 constexpr int kMaxCtas = 1024;         // partial weight gradients are sized for this many
-constexpr int kUnroll = 4;             // rows in flight per lane
 
 struct NormSide {
     const void* x; const void* dy;     // dy: backward only
@@ -44,43 +45,26 @@ struct NormArgs {
     const float* inv_freq; const int32_t* positions;
     int T, d, rot, slab, slabs;        // heads of one unit of work, units per token
     int64_t tokens;
-    int interleaved;
     float m, eps;
     float* partial;                    // [CTAs][2][d], backward with weights only
 };
 
-template <typename T> struct Vec8;
-template <> struct Vec8<__nv_bfloat16> {
-    uint4 raw;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
-        __align__(16) __nv_bfloat162 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+// Four consecutive channels as loaded, and as fp32.
+template <typename T> struct Vec4;
+template <> struct Vec4<__nv_bfloat16> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = __ldcs(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = unpack_bf16(raw.x); x[1] = unpack_bf16(raw.y); }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&x)[2]) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y));
     }
 };
-template <> struct Vec8<float> {
-    float4 lo, hi;
-    __device__ __forceinline__ void load(const float* p) {
-        lo = __ldcs(reinterpret_cast<const float4*>(p));
-        hi = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
-        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+template <> struct Vec4<float> {
+    float4 raw;
+    __device__ __forceinline__ void load(const float* p) { raw = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = make_float2(raw.x, raw.y); x[1] = make_float2(raw.z, raw.w); }
+    static __device__ __forceinline__ void store(float* p, const float2 (&x)[2]) {
+        *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
     }
 };
 
@@ -91,56 +75,38 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Turns this lane's eight channels by (c, s).  Pairs lie in one lane
-// (interleaved) or `hop` lanes apart (first half with second half).  All lanes of
-// the warp call it; `in` says whether this lane's channels turn.
-__device__ __forceinline__ void turn(float (&x)[8], const float (&c)[8], const float (&s)[8], bool in, int interleaved,
-                                     int partner, bool second) {
-    if (interleaved) {
-        if (in) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = fmaf(a, c[i], -b * s[i]);
-                x[2 * i + 1] = fmaf(b, c[i], a * s[i]);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(0xffffffffu, x[i], partner);
-        if (in) x[i] = fmaf(x[i], c[i], (second ? other : -other) * s[i]);
-    }
+// The other channel of each pair of a lane's 2 x 4 channels.
+template <bool INTER>
+__device__ __forceinline__ float2 other_of(const float2 (&x)[4], int i) {
+    return INTER ? make_float2(x[i].y, x[i].x) : x[i ^ 2];
 }
 
-template <typename T, int LPR, bool BWD>
-__global__ void __launch_bounds__(kWarps * 32)
+template <typename T, int LPR, bool BWD, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3)
 qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
 {
     constexpr int RPW = 32 / LPR;
-    __shared__ float angle[kWarps][2][128];
+    // rows in flight per lane, as registers allow for three (backward two) CTAs an SM
+    constexpr int kUnroll = 8 / (int)sizeof(T);
+    __shared__ __align__(8) float angle[kWarps][2][128];
     __shared__ float red[BWD ? kWarps : 1][2][256];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = lane / LPR, e0 = 8 * (lane % LPR);
-    const bool mine = e0 < a.d;                    // lanes past the row's end only take part in shuffles
+    const int sub = lane / LPR, l = lane % LPR;
+    const bool mine = 8 * l < a.d;                 // lanes past the row's end only take part in sums
     const int half = a.rot / 2;
-    const bool in = e0 < a.rot, second = e0 >= half;
-    const int partner = (in && !a.interleaved) ? (second ? lane - half / 8 : lane + half / 8) : lane;
+    // first channels of the lane's two groups
+    const bool paired = !INTER && 4 * l < half;    // (j, j + half)
+    const int e0 = INTER ? 8 * l : paired ? 4 * l : a.rot + 8 * l - 2 * half;
+    const int e1 = paired ? e0 + half : e0 + 4;
+    const bool turns = mine && (INTER ? e0 < a.rot : paired);
+
+    float2 dw[BWD ? 2 : 1][4];                     // gradients of the weights of queries and keys
+#pragma unroll
+    for (int q = 0; q < (BWD ? 2 : 1); ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[q][i] = make_float2(0.f, 0.f);
+
     const int heads = a.side[0].heads + a.side[1].heads;
-
-    float w[2][8], dw[2][8];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[q][i] = (mine && a.side[q].w) ? a.side[q].w[e0 + i] : 1.f;
-            dw[q][i] = 0.f;
-        }
-    float c[8], s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-
     const int64_t units = a.tokens * a.slabs, stride = (int64_t)gridDim.x * kWarps;
     for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += stride) {
         const int64_t tok = u / a.slabs;
@@ -150,70 +116,121 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
             const double pos = a.positions ? (double)a.positions[tok] : (double)t;
             __syncwarp();
             for (int j = lane; j < half; j += 32) {
-                double turns = pos * (double)a.inv_freq[j] * 0.15915494309189535;   // 1 / (2 pi)
-                turns -= rint(turns);
+                double rounds = pos * (double)a.inv_freq[j] * 0.15915494309189535;   // 1 / (2 pi)
+                rounds -= rint(rounds);
                 float sn, cs;
-                sincospif(2.f * (float)turns, &sn, &cs);
+                sincospif(2.f * (float)rounds, &sn, &cs);
                 angle[warp][0][j] = cs;
                 angle[warp][1][j] = BWD ? -sn : sn;
             }
             __syncwarp();
-            if (in) {
-                const int j0 = a.interleaved ? e0 / 2 : (second ? e0 - half : e0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < 4 || !a.interleaved) { c[i] = angle[warp][0][j0 + i]; s[i] = angle[warp][1][j0 + i]; }
-            }
         }
-        for (int r0 = first; r0 < end; r0 += RPW * kUnroll) {
-            Vec8<T> xv[kUnroll], gv[BWD ? kUnroll : 1];
 #pragma unroll
-            for (int n = 0; n < kUnroll; ++n) {     // all loads first
-                const int r = r0 + n * RPW + sub;
-                if (r < end && mine) {
-                    const int q = r >= a.side[0].heads, hd = r - (q ? a.side[0].heads : 0);
-                    const NormSide& z = a.side[q];
-                    xv[n].load(static_cast<const T*>(z.x) + b * z.sb + t * z.st + hd * z.sh + e0);
-                    if constexpr (BWD)
-                        gv[n].load(static_cast<const T*>(z.dy) + (tok * z.heads + hd) * (int64_t)a.d + e0);
+        for (int q = 0; q < 2; ++q) {
+            const NormSide& z = a.side[q];
+            const int shift = q ? a.side[0].heads : 0;
+            const int lo = max(first - shift, 0), hi = min(end - shift, z.heads);    // this unit's heads of this side
+            if (lo >= hi) continue;
+            const T* x_tok = static_cast<const T*>(z.x) + b * z.sb + t * z.st;
+            const T* g_tok = BWD ? static_cast<const T*>(z.dy) + tok * z.heads * (int64_t)a.d : nullptr;
+            T* out_tok = static_cast<T*>(z.out) + tok * z.heads * (int64_t)a.d;
+            // y = n c + (other of n's pair) s, with c and s times the weights in the forward
+            float2 w[4], c[4], s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = (i < 2 ? e0 : e1) + 2 * (i & 1);
+                w[i] = (mine && z.w) ? *reinterpret_cast<const float2*>(z.w + e) : make_float2(1.f, 1.f);
+                c[i] = make_float2(1.f, 1.f);
+                s[i] = make_float2(0.f, 0.f);
+                if (!turns) continue;
+                if constexpr (INTER) {             // pair (x, y) of one float2
+                    const float cs = angle[warp][0][e / 2], sn = angle[warp][1][e / 2];
+                    c[i] = make_float2(cs, cs);
+                    s[i] = make_float2(-sn, sn);
+                } else {                           // pairs (x[0], x[2]), (x[1], x[3])
+                    const int j = e0 + 2 * (i & 1);
+                    const float2 sn = *reinterpret_cast<const float2*>(&angle[warp][1][j]);
+                    c[i] = *reinterpret_cast<const float2*>(&angle[warp][0][j]);
+                    s[i] = i < 2 ? make_float2(-sn.x, -sn.y) : sn;
                 }
             }
+            if constexpr (!BWD) {
 #pragma unroll
-            for (int n = 0; n < kUnroll; ++n) {
-                if (r0 + n * RPW >= end) break;     // uniform over the warp
-                const int r = r0 + n * RPW + sub;
-                const bool on = r < end && mine;
-                const int q = r >= a.side[0].heads, hd = r - (q ? a.side[0].heads : 0);
-                float x[8], ss = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    c[i] = mul2(w[i], c[i]);
+                    s[i] = mul2(other_of<INTER>(w, i), s[i]);
+                }
+            }
+            for (int r0 = lo; r0 < hi; r0 += RPW * kUnroll) {
+                Vec4<T> xv[kUnroll][2], gv[BWD ? kUnroll : 1][2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
-                if (on) xv[n].get(x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                ss = row_sum<LPR>(ss);
-                const float rs = rsqrtf(fmaf(ss, a.m, a.eps));
-                if constexpr (!BWD) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= rs * (q ? w[1][i] : w[0][i]);
-                    if (a.rot) turn(x, c, s, in, a.interleaved, partner, second);
-                    if (on) Vec8<T>::store(static_cast<T*>(a.side[q].out) + (tok * a.side[q].heads + hd) * (int64_t)a.d + e0, x);
-                } else {
-                    float g[8], dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = 0.f;
-                    if (on) gv[n].get(g);
-                    if (a.rot) turn(g, c, s, in, a.interleaved, partner, second);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p = g[i] * x[i] * rs;
-                        if (q) dw[1][i] += p; else dw[0][i] += p;
-                        g[i] *= q ? w[1][i] : w[0][i];
-                        dot = fmaf(g[i], x[i], dot);
+                for (int n = 0; n < kUnroll; ++n) {     // all loads first
+                    const int r = r0 + n * RPW + sub;
+                    if (r < hi && mine) {
+                        const T* p = x_tok + r * z.sh;
+                        xv[n][0].load(p + e0);
+                        xv[n][1].load(p + e1);
+                        if constexpr (BWD) {
+                            const T* g = g_tok + r * (int64_t)a.d;
+                            gv[n][0].load(g + e0);
+                            gv[n][1].load(g + e1);
+                        }
                     }
-                    dot = row_sum<LPR>(dot) * a.m * rs * rs;
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = rs * fmaf(-dot, x[i], g[i]);
-                    if (on) Vec8<T>::store(static_cast<T*>(a.side[q].out) + (tok * a.side[q].heads + hd) * (int64_t)a.d + e0, g);
+                for (int n = 0; n < kUnroll; ++n) {
+                    if (r0 + n * RPW >= hi) break;      // uniform over the warp
+                    const int r = r0 + n * RPW + sub;
+                    const bool on = r < hi && mine;
+                    float2 x[4], h[4];
+                    if (on) {
+                        xv[n][0].get(*reinterpret_cast<float2(*)[2]>(&x[0]));
+                        xv[n][1].get(*reinterpret_cast<float2(*)[2]>(&x[2]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = make_float2(0.f, 0.f);
+                    }
+                    float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+                    const float rs = rsqrtf(fmaf(row_sum<LPR>(ss.x + ss.y), a.m, a.eps));
+                    const float2 rr = make_float2(rs, rs);
+                    if constexpr (!BWD) {
+                        // a channel that does not turn takes nothing from its neighbour, be it infinite
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = mul2(x[i], c[i]);
+                            h[i] = mul2(rr, turns ? fma2(other_of<INTER>(x, i), s[i], y) : y);
+                        }
+                    } else {
+                        float2 g[4], dot = make_float2(0.f, 0.f);
+                        if (on) {
+                            gv[n][0].get(*reinterpret_cast<float2(*)[2]>(&g[0]));
+                            gv[n][1].get(*reinterpret_cast<float2(*)[2]>(&g[2]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) g[i] = make_float2(0.f, 0.f);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = mul2(g[i], c[i]);
+                            h[i] = turns ? fma2(other_of<INTER>(g, i), s[i], y) : y;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            dw[q][i] = fma2(mul2(h[i], x[i]), rr, dw[q][i]);
+                            h[i] = mul2(h[i], w[i]);
+                            dot = fma2(h[i], x[i], dot);
+                        }
+                        const float k = -row_sum<LPR>(dot.x + dot.y) * a.m * rs * rs;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[i] = mul2(rr, fma2(make_float2(k, k), x[i], h[i]));
+                    }
+                    if (on) {
+                        T* out = out_tok + r * (int64_t)a.d;
+                        Vec4<T>::store(out + e0, *reinterpret_cast<const float2(*)[2]>(&h[0]));
+                        Vec4<T>::store(out + e1, *reinterpret_cast<const float2(*)[2]>(&h[2]));
+                    }
                 }
             }
         }
@@ -225,11 +242,18 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float v = dw[q][i];
+            for (int i = 0; i < 4; ++i) {
+                float2 v = dw[q][i];
 #pragma unroll
-                for (int off = LPR; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                if (sub == 0 && mine) red[warp][q][e0 + i] = v;
+                for (int off = LPR; off < 32; off <<= 1) {
+                    v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+                    v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+                }
+                const int e = (i < 2 ? e0 : e1) + 2 * (i & 1);
+                if (sub == 0 && mine) {
+                    red[warp][q][e] = v.x;
+                    red[warp][q][e + 1] = v.y;
+                }
             }
         __syncthreads();
         for (int e = threadIdx.x; e < 2 * a.d; e += kWarps * 32) {
@@ -261,12 +285,17 @@ norm_weight_grad_kernel(const float* __restrict__ partial, int ctas, int d, floa
     }
 }
 
-template <typename T, bool BWD>
+template <typename T, bool BWD, bool INTER>
 cudaError_t launch_norm_t(const NormArgs& a, int ctas, cudaStream_t s) {
-    auto kern = a.d <= 64 ? qk_norm_rope_kernel<T, 8, BWD>
-              : a.d <= 128 ? qk_norm_rope_kernel<T, 16, BWD> : qk_norm_rope_kernel<T, 32, BWD>;
+    auto kern = a.d <= 64 ? qk_norm_rope_kernel<T, 8, BWD, INTER>
+              : a.d <= 128 ? qk_norm_rope_kernel<T, 16, BWD, INTER> : qk_norm_rope_kernel<T, 32, BWD, INTER>;
     kern<<<ctas, kWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_norm(const NormArgs& a, bool bwd, bool interleaved, int ctas, cudaStream_t s) {
+    if (bwd) return interleaved ? launch_norm_t<T, true, true>(a, ctas, s) : launch_norm_t<T, true, false>(a, ctas, s);
+    return interleaved ? launch_norm_t<T, false, true>(a, ctas, s) : launch_norm_t<T, false, false>(a, ctas, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -300,8 +329,8 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
         if (!q || !k || !oq || !ok_ || !qs || !ks || (bwd && (!dyq || !dyk)) || (rot && !inv_freq))
             return (kda_status)set_error(KDA_ERR_INVALID_ARG, "null pointer");
         const int per16 = dtype == KDA_BF16 ? 8 : 4;
-        if (!aligned16(q) || !aligned16(k) || !aligned16(oq) || !aligned16(ok_) || (bwd && (!aligned16(dyq) || !aligned16(dyk))))
-            return (kda_status)set_error(KDA_ERR_INVALID_ARG, "queries, keys and outputs must be 16-byte aligned");
+        if (!aligned16(q) || !aligned16(k) || !aligned16(oq) || !aligned16(ok_) || !aligned16(wq) || !aligned16(wk) || (bwd && (!aligned16(dyq) || !aligned16(dyk))))
+            return (kda_status)set_error(KDA_ERR_INVALID_ARG, "queries, keys, weights and outputs must be 16-byte aligned");
         for (int i = 0; i < 3; ++i)
             if (qs[i] % per16 || ks[i] % per16)
                 return (kda_status)set_error(KDA_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
@@ -319,7 +348,7 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     a.side[0] = {q, dyq, oq, wq, qs ? qs[0] : 0, qs ? qs[1] : 0, qs ? qs[2] : 0, Hq};
     a.side[1] = {k, dyk, ok_, wk, ks ? ks[0] : 0, ks ? ks[1] : 0, ks ? ks[2] : 0, Hk};
     a.inv_freq = inv_freq; a.positions = positions;
-    a.T = T > 0 ? T : 1; a.d = d; a.rot = rot; a.tokens = tokens; a.interleaved = interleaved != 0;
+    a.T = T > 0 ? T : 1; a.d = d; a.rot = rot; a.tokens = tokens;
     a.m = norm == KDA_NORM_RMS ? 1.f / (float)d : 1.f;
     a.eps = eps;
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
@@ -331,14 +360,11 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     a.slab = (a.slab + rpw - 1) / rpw * rpw;
     a.slabs = (heads + a.slab - 1) / a.slab;
     const int64_t want = (tokens * a.slabs + kWarps - 1) / kWarps;
-    const int ctas = (int)std::min<int64_t>(want, std::min(kMaxCtas, sms * (bwd ? 4 : 6)));
+    const int ctas = (int)std::min<int64_t>(want, std::min(kMaxCtas, sms * (bwd ? 2 : 3)));
     if (e == cudaSuccess && ctas > 0) {
-        if (dtype == KDA_BF16)
-            e = bwd ? launch_norm_t<__nv_bfloat16, true>(a, ctas, static_cast<cudaStream_t>(stream))
-                    : launch_norm_t<__nv_bfloat16, false>(a, ctas, static_cast<cudaStream_t>(stream));
-        else
-            e = bwd ? launch_norm_t<float, true>(a, ctas, static_cast<cudaStream_t>(stream))
-                    : launch_norm_t<float, false>(a, ctas, static_cast<cudaStream_t>(stream));
+        e = dtype == KDA_BF16
+            ? launch_norm<__nv_bfloat16>(a, bwd, interleaved != 0, ctas, static_cast<cudaStream_t>(stream))
+            : launch_norm<float>(a, bwd, interleaved != 0, ctas, static_cast<cudaStream_t>(stream));
     }
     if (e == cudaSuccess && sums) {
         norm_weight_grad_kernel<<<dim3((d + 31) / 32, 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(

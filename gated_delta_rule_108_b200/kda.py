@@ -448,31 +448,67 @@ def recurrent_step(q, k, v, log_alpha, beta, state, o=None, stream=None) -> torc
 
 
 # ------------------------------------------- linear attention, decay per head --
+# These calls are short enough that the host's part shows, so the checks run over
+# all tensors at once and name what is wrong only where something is.
 def _on(device):
     """The library launches on the current device; make that the tensors' device
     for the call where it is another."""
-    return (contextlib.nullcontext() if torch.cuda.current_device() == device.index
-            else torch.cuda.device(device))
+    return (_HERE_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device))
 
 
-def _log_decay(log_decay, H: int, device) -> None:
-    if log_decay is not None:
-        _shape(log_decay, "log_decay", (H,))
-        _need(log_decay, "log_decay", torch.float32, device)
+_HERE_DEVICE = contextlib.nullcontext()
+
+
+def _loaded():
+    """:func:`lib` without its lock, once it is loaded."""
+    return _lib if _lib is not None else lib()
+
+
+def _raw_stream(stream, device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _verify(device, specs) -> None:
+    """Each (tensor or None, name, shape, dtype) is contiguous, of that shape and
+    type, on ``device``, a GPU; a shape or dtype of None may be any."""
+    for t, _, shape, dtype in specs:
+        if t is not None and not ((shape is None or t.shape == shape) and (dtype is None or t.dtype is dtype)
+                                  and t.device == device and t.is_contiguous()):
+            break
+    else:
+        if device.type == "cuda":
+            return
+    for t, name, shape, _ in specs:
+        if shape is not None:
+            _shape(t, name, shape)
+    for t, name, _, dtype in specs:
+        if t is not None:
+            _need(t, name, dtype, device)
+
+
+def _run_status(status: int, workspace, stream, device, check: Optional[bool]) -> None:
+    if status != KDA_OK:
+        _check(status)
+    if check if check is not None else _validate_default():
+        _check_device_status(workspace, stream if stream is not None else torch.cuda.current_stream(device))
 
 
 def linear_chunk_fwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
                                     num_seqs: int, varlen: bool, dtype: torch.dtype) -> int:
     """Workspace bytes ``linear_chunk_fwd`` needs (``kda_linear_chunk_fwd_workspace_size``)."""
     code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    return int(lib().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, num_seqs, int(bool(varlen)), code))
+    return _loaded().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, num_seqs, int(varlen), code)
 
 
 def linear_chunk_bwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
                                     num_seqs: int, varlen: bool, dtype: torch.dtype) -> int:
     """Workspace bytes ``linear_chunk_bwd`` needs (``kda_linear_chunk_bwd_workspace_size``)."""
     code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    return int(lib().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, num_seqs, int(bool(varlen)), code))
+    return _loaded().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, num_seqs, int(varlen), code)
 
 
 def linear_chunk_fwd(q, k, v, log_decay=None, initial_state=None, cu_seqlens=None,
@@ -489,41 +525,33 @@ def linear_chunk_fwd(q, k, v, log_decay=None, initial_state=None, cu_seqlens=Non
     _dims(q, "q", 4)
     _dims(v, "v", 4)
     B, T, H, dk = q.shape
-    dv = v.shape[-1]
+    dv = v.shape[3]
     N = _num_seqs(B, cu_seqlens)
-    for t, n, shape in ((k, "k", (B, T, H, dk)), (v, "v", (B, T, H, dv)),
-                        (initial_state, "initial_state", (N, H, dk, dv)), (o, "o", (B, T, H, dv)),
-                        (final_state, "final_state", (N, H, dk, dv))):
-        _shape(t, n, shape)
-    dev = q.device
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, n, q.dtype, dev)
-    _log_decay(log_decay, H, dev)
-    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (initial_state, "initial_state", torch.float32),
-                     (o, "o", q.dtype), (final_state, "final_state", torch.float32),
-                     (workspace, "workspace", None)):
-        if t is not None:
-            _need(t, n, dt, dev)
+    dev, dtype, f32, state = q.device, q.dtype, torch.float32, (N, H, dk, dv)
+    _verify(dev, ((q, "q", None, dtype), (k, "k", (B, T, H, dk), dtype), (v, "v", (B, T, H, dv), dtype),
+                  (log_decay, "log_decay", (H,), f32), (initial_state, "initial_state", state, f32),
+                  (cu_seqlens, "cu_seqlens", None, torch.int32), (o, "o", (B, T, H, dv), dtype),
+                  (final_state, "final_state", state, f32), (workspace, "workspace", None, None)))
     code = _dtype_code(q)
     made = []
     if o is None:
-        o = torch.empty(B, T, H, dv, dtype=q.dtype, device=dev)
+        o = torch.empty((B, T, H, dv), dtype=dtype, device=dev)
         made.append(o)
     if final_state is None and output_final_state:
-        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
+        final_state = torch.empty(state, dtype=f32, device=dev)
         made.append(final_state)
     if workspace is None:
-        ws_bytes = linear_chunk_fwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, q.dtype)
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        size = _loaded().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, code)
+        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _used_on(stream, dev, *made)
+    if stream is not None:
+        _used_on(stream, dev, *made)
     with _on(dev):
-        _check(lib().kda_linear_chunk_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(cu_seqlens),
-            B, T, H, dk, dv, N, code, _ptr(o), _ptr(final_state),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
-        if check if check is not None else _validate_default():
-            _check_device_status(workspace, stream)
+        status = _loaded().kda_linear_chunk_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(log_decay), _addr(initial_state), _addr(cu_seqlens),
+            B, T, H, dk, dv, N, code, o.data_ptr(), _addr(final_state),
+            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+        _run_status(status, workspace, stream, dev, check)
     return o, final_state
 
 
@@ -539,38 +567,29 @@ def linear_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=
     _dims(q, "q", 4)
     _dims(v, "v", 4)
     B, T, H, dk = q.shape
-    dv = v.shape[-1]
+    dv = v.shape[3]
     N = _num_seqs(B, cu_seqlens)
-    for t, n, shape in ((k, "k", (B, T, H, dk)), (v, "v", (B, T, H, dv)), (d_o, "d_o", (B, T, H, dv)),
-                        (initial_state, "initial_state", (N, H, dk, dv)),
-                        (d_final_state, "d_final_state", (N, H, dk, dv))):
-        _shape(t, n, shape)
-    dev = q.device
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
-        _need(t, n, q.dtype, dev)
-    _log_decay(log_decay, H, dev)
-    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (initial_state, "initial_state", torch.float32),
-                     (d_final_state, "d_final_state", torch.float32), (workspace, "workspace", None)):
-        if t is not None:
-            _need(t, n, dt, dev)
+    dev, dtype, f32, state = q.device, q.dtype, torch.float32, (N, H, dk, dv)
+    _verify(dev, ((q, "q", None, dtype), (k, "k", (B, T, H, dk), dtype), (v, "v", (B, T, H, dv), dtype),
+                  (d_o, "d_o", (B, T, H, dv), dtype), (log_decay, "log_decay", (H,), f32),
+                  (initial_state, "initial_state", state, f32), (d_final_state, "d_final_state", state, f32),
+                  (cu_seqlens, "cu_seqlens", None, torch.int32), (workspace, "workspace", None, None)))
     code = _dtype_code(q)
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-         "dS0": (torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)
-                 if output_d_initial_state else None)}
+         "dS0": torch.empty(state, dtype=f32, device=dev) if output_d_initial_state else None}
     made = list(g.values())
     if workspace is None:
-        ws_bytes = linear_chunk_bwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, q.dtype)
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        size = _loaded().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, code)
+        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _used_on(stream, dev, *made)
+    if stream is not None:
+        _used_on(stream, dev, *made)
     with _on(dev):
-        _check(lib().kda_linear_chunk_bwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_o),
-            _ptr(d_final_state), B, T, H, dk, dv, N, code, _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
-            _ptr(g["dS0"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _stream_ptr(stream, dev)))
-        if check if check is not None else _validate_default():
-            _check_device_status(workspace, stream)
+        status = _loaded().kda_linear_chunk_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(log_decay), _addr(initial_state), _addr(cu_seqlens),
+            d_o.data_ptr(), _addr(d_final_state), B, T, H, dk, dv, N, code, g["dq"].data_ptr(), g["dk"].data_ptr(),
+            g["dv"].data_ptr(), _addr(g["dS0"]), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+        _run_status(status, workspace, stream, dev, check)
     return g
 
 
@@ -584,76 +603,72 @@ def linear_recurrent_step(q, k, v, log_decay, state, o=None, stream=None) -> tor
     _dims(q, "q", 3)
     _dims(v, "v", 3)
     B, H, dk = q.shape
-    dv = v.shape[-1]
-    for t, n, shape in ((k, "k", (B, H, dk)), (v, "v", (B, H, dv)), (state, "state", (B, H, dk, dv)),
-                        (o, "o", (B, H, dv))):
-        _shape(t, n, shape)
-    dev = q.device
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, n, q.dtype, dev)
-    _log_decay(log_decay, H, dev)
-    _need(state, "state", torch.float32, dev)
+    dv = v.shape[2]
+    dev, dtype, f32 = q.device, q.dtype, torch.float32
+    _verify(dev, ((q, "q", None, dtype), (k, "k", (B, H, dk), dtype), (v, "v", (B, H, dv), dtype),
+                  (log_decay, "log_decay", (H,), f32), (state, "state", (B, H, dk, dv), f32),
+                  (o, "o", (B, H, dv), dtype)))
     code = _dtype_code(q)
-    if o is not None:
-        _need(o, "o", q.dtype, dev)
-    else:
-        o = torch.empty(B, H, dv, dtype=q.dtype, device=dev)
-        _used_on(stream, dev, o)
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=dtype, device=dev)
+        if stream is not None:
+            _used_on(stream, dev, o)
     with _on(dev):
-        _check(lib().kda_linear_recurrent_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), B, H, dk, dv, code, _ptr(o),
-            _stream_ptr(stream, dev)))
+        status = _loaded().kda_linear_recurrent_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(log_decay), state.data_ptr(), B, H, dk, dv, code,
+            o.data_ptr(), _raw_stream(stream, dev))
+    if status != KDA_OK:
+        _check(status)
     return o
 
 
 # ------------------------------------------------ norm and rotation of q and k --
-def _need_rows(t: torch.Tensor, name: str, dtype, device):
-    """Like :func:`_need` for rows that may lie apart: only channels are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
+_INT64x3 = ctypes.c_int64 * 3
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device):
+    """Element strides of batch, token and head of rows that may lie apart: only
+    their channels are contiguous."""
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    s, n = t.stride(), t.shape
+    if s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
+    # a dimension of one element is never stepped over, whatever stride torch gives it
+    head = s[-2] if n[-2] != 1 else 0
+    first = s[0] if n[0] != 1 else 0
+    return _INT64x3(first, s[1] if len(n) == 4 and n[1] != 1 else 0, head)
 
 
-def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm, cotangents=()):
+def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm, more):
     """Checks the arguments the norm and its gradients share; returns the sizes
-    (B, T, Hq, Hk, d, rotary_dim), the norm's code and the strides."""
-    if q.dim() not in (3, 4):
+    (B, T, Hq, Hk, d, rotary_dim), the norm's code and the strides.  ``more`` names
+    the tensors shaped like q and like k."""
+    ndim = q.dim()
+    if ndim not in (3, 4):
         raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(q.shape)}")
-    _dims(k, "k", q.dim())
-    lead, Hq, d = tuple(q.shape[:-2]), q.shape[-2], q.shape[-1]
-    Hk = k.shape[-2]
-    _shape(k, "k", (*lead, Hk, d))
-    B, T = lead if q.dim() == 4 else (lead[0], 1)
-    for t, n, shape in ((q_weight, "q_weight", (d,)), (k_weight, "k_weight", (d,)), (positions, "positions", lead),
-                        *cotangents):
-        _shape(t, n, shape)
+    _dims(k, "k", ndim)
+    qshape, kshape = q.shape, k.shape
+    lead, Hq, Hk, d = qshape[:-2], qshape[-2], kshape[-2], qshape[-1]
+    if kshape[:-2] != lead or kshape[-1] != d:
+        _shape(k, "k", (*lead, Hk, d))
+    B, T = lead if ndim == 4 else (lead[0], 1)
     rot = 0
     if inv_freq is not None:
         _dims(inv_freq, "inv_freq", 1)
-        rot = 2 * inv_freq.numel()
-        if q.dim() == 3 and positions is None:
+        rot = 2 * inv_freq.shape[0]
+        if ndim == 3 and positions is None:
             raise ValueError("a rotation of single tokens needs their positions")
-    if norm not in ("rms", "l2"):
+    code = {"rms": KDA_NORM_RMS, "l2": KDA_NORM_L2}.get(norm)
+    if code is None:
         raise ValueError(f"norm must be 'rms' or 'l2', got {norm!r}")
-    dev = q.device
-    _need_rows(q, "q", q.dtype, dev)
-    _need_rows(k, "k", q.dtype, dev)
-    for t, n, dt in ((q_weight, "q_weight", torch.float32), (k_weight, "k_weight", torch.float32),
-                     (inv_freq, "inv_freq", torch.float32), (positions, "positions", torch.int32)):
-        if t is not None:
-            _need(t, n, dt, dev)
-
-    def strides(t):
-        s = t.stride() if t.dim() == 4 else (t.stride(0), 0, t.stride(1))
-        # a dimension of one element is never stepped over, whatever stride torch gives it
-        return (ctypes.c_int64 * 3)(*[0 if n == 1 else x for x, n in zip(s, (B, T, t.shape[-2]))])
-
-    return (B, T, Hq, Hk, d, rot), (KDA_NORM_RMS if norm == "rms" else KDA_NORM_L2), strides(q), strides(k)
+    dev, dtype, f32 = q.device, q.dtype, torch.float32
+    _verify(dev, ((q_weight, "q_weight", (d,), f32), (k_weight, "k_weight", (d,), f32),
+                  (inv_freq, "inv_freq", None, f32), (positions, "positions", lead, torch.int32),
+                  *[(t, n, qshape if of_q else kshape, dtype) for t, n, of_q in more]))
+    return (B, T, Hq, Hk, d, rot), code, _rows(q, "q", dtype, dev), _rows(k, "k", dtype, dev)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, norm: str = "l2",
@@ -670,23 +685,24 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
     [B, T] ([B] for single tokens), None: 0 .. T-1.  Returns (q_out, k_out),
     contiguous and of the inputs' dtype.
     """
-    shapes = (((*q.shape,), q_out, "q_out"), ((*k.shape,), k_out, "k_out"))
-    (B, T, Hq, Hk, d, rot), code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
-                                                      [(t, n, s) for s, t, n in shapes])
+    sizes, code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
+                                     ((q_out, "q_out", True), (k_out, "k_out", False)))
     dev, dt = q.device, _dtype_code(q)
     made = []
-    for s, t, n in shapes:
-        if t is not None:
-            _need(t, n, q.dtype, dev)
-        else:
-            made.append(torch.empty(s, dtype=q.dtype, device=dev))
-    _used_on(stream, dev, *made)
-    k_out = made.pop() if k_out is None else k_out
-    q_out = made.pop() if q_out is None else q_out
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        made.append(q_out)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        made.append(k_out)
+    if stream is not None:
+        _used_on(stream, dev, *made)
     with _on(dev):
-        _check(lib().kda_qk_norm_rope(
-            _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), B, T, Hq, Hk, d, rot,
-            qs, ks, dt, code, float(eps), int(bool(interleaved)), _ptr(q_out), _ptr(k_out), _stream_ptr(stream, dev)))
+        status = _loaded().kda_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), *sizes,
+            qs, ks, dt, code, eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(stream, dev))
+    if status != KDA_OK:
+        _check(status)
     return q_out, k_out
 
 
@@ -696,12 +712,9 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, inv_f
     """Gradients of :func:`qk_norm_rope` (``kda_qk_norm_rope_bwd``): q, k its inputs,
     d_q_out, d_k_out the cotangents of its outputs.  Returns a dict with dq, dk
     (contiguous) and dq_weight, dk_weight [d] fp32 (None without that weight)."""
-    (B, T, Hq, Hk, d, rot), code, qs, ks = _norm_args(
-        q, k, q_weight, k_weight, inv_freq, positions, norm,
-        [(d_q_out, "d_q_out", tuple(q.shape)), (d_k_out, "d_k_out", tuple(k.shape))])
+    sizes, code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
+                                     ((d_q_out, "d_q_out", True), (d_k_out, "d_k_out", False)))
     dev, dt = q.device, _dtype_code(q)
-    for t, n in ((d_q_out, "d_q_out"), (d_k_out, "d_k_out")):
-        _need(t, n, q.dtype, dev)
     g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
          "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
          "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
@@ -709,13 +722,16 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, inv_f
     if workspace is not None:
         _need(workspace, "workspace", None, dev)
     elif q_weight is not None or k_weight is not None:
-        workspace = torch.empty(max(int(lib().kda_qk_norm_rope_bwd_workspace_size(d)), 1), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(_loaded().kda_qk_norm_rope_bwd_workspace_size(sizes[4]), 1), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _used_on(stream, dev, *made)
+    if stream is not None:
+        _used_on(stream, dev, *made)
     with _on(dev):
-        _check(lib().kda_qk_norm_rope_bwd(
-            _ptr(q), _ptr(k), _ptr(d_q_out), _ptr(d_k_out), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-            _ptr(positions), B, T, Hq, Hk, d, rot, qs, ks, dt, code, float(eps), int(bool(interleaved)),
-            _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
+        status = _loaded().kda_qk_norm_rope_bwd(
+            q.data_ptr(), k.data_ptr(), d_q_out.data_ptr(), d_k_out.data_ptr(), _addr(q_weight), _addr(k_weight),
+            _addr(inv_freq), _addr(positions), *sizes, qs, ks, dt, code, eps, interleaved, g["dq"].data_ptr(),
+            g["dk"].data_ptr(), _addr(g["dq_weight"]), _addr(g["dk_weight"]), _addr(workspace),
+            0 if workspace is None else workspace.nbytes, _raw_stream(stream, dev))
+    if status != KDA_OK:
+        _check(status)
     return g

@@ -417,7 +417,7 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
  *              of a head contiguous; q_strides / k_strides are the element strides
  *              of batch, token and head (host arrays, multiples of 16 bytes), so a
  *              slice of a joint projection is taken as it lies
- *  q_weight, k_weight [d] fp32, or NULL for ones
+ *  q_weight, k_weight [d] fp32, 16-byte aligned, or NULL for ones
  *  inv_freq    [rotary_dim / 2] fp32 (NULL only with rotary_dim = 0)
  *  positions   [B, T] int32, or NULL for 0 .. T-1 in every row of the batch
  *  d           a multiple of 8 up to 256; rotary_dim a multiple of 16 up to d
