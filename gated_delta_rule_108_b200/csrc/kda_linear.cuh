@@ -100,7 +100,7 @@ struct LinArgs {
     LinMap map;
     int max_segments;             // host bound on map.segments()
     bool split;                   // some sequence may have more than one segment
-    int roles;
+    int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role
     LinRole role[kLinMaxRoles];
     WsHeader* hdr;
     bool reset;                   // the launch starts the call: block 0 clears the status

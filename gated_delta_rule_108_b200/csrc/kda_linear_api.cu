@@ -120,7 +120,8 @@ LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, in
     return a;
 }
 
-// All roles of `a`; those with the same (D1, D2) share a launch.
+// The launches of a call: the segment table of a packed batch, the segments' sums
+// and their scan where sequences are cut, the chunk kernel.
 cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     LinArgs all = a;
     for (int i = 0; i < all.roles; ++i)
@@ -129,28 +130,14 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     if (all.map.cu) e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
     else if (p.max_segments == 0) e = cudaMemsetAsync(all.hdr, 0, sizeof(WsHeader), all.stream);
     if (p.max_segments == 0) return e;
+    auto pass = [&](bool states_only) { return all.bf16 ? launch_linear_tc(all, states_only) : launch_linear_simt(all, states_only); };
     all.reset = true;
-    auto pass = [&](bool states_only) {
-        bool done[kLinMaxRoles] = {};
-        for (int i = 0; i < all.roles && e == cudaSuccess; ++i) {
-            if (done[i]) continue;
-            LinArgs one = all;
-            one.roles = 0;
-            for (int j = i; j < all.roles; ++j)
-                if (all.dim[all.role[j].a] == all.dim[all.role[i].a] && all.dim[all.role[j].c] == all.dim[all.role[i].c]) {
-                    one.role[one.roles++] = all.role[j];
-                    done[j] = true;
-                }
-            e = a.bf16 ? launch_linear_tc(one, states_only) : launch_linear_simt(one, states_only);
-            all.reset = false;
-        }
-    };
     if (p.split && e == cudaSuccess) {
-        pass(true);
+        e = pass(true);
+        all.reset = false;
         if (e == cudaSuccess) e = launch_linear_scan(all);
     }
-    if (e == cudaSuccess) pass(false);
-    return e;
+    return e == cudaSuccess ? pass(false) : e;
 }
 
 }  // namespace

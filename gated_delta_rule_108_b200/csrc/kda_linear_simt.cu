@@ -12,6 +12,8 @@
 // with n_r = r + 1, m_i = L - 1 - i first to last and n_r = L - 1 - r,
 // m_i = i + 1 last to first (a cotangent decays when it leaves its token, a state
 // before it enters).
+#include <algorithm>
+
 #include "kda_linear.cuh"
 #include "ptx.cuh"
 
@@ -165,19 +167,16 @@ __device__ __forceinline__ void axpy(float2 (&y)[2], float p, const float4& c) {
 // 32 instructions per 8 16-byte shared-memory reads); the next chunk's tiles arrive
 // by cp.async meanwhile, rows past a segment's end as zeros.
 template <int D1, int D2>
-__global__ void __launch_bounds__(256)
-linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
+__device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, int x, int states_only)
 {
     using Sm = LinSimtSmem<D1>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
-    if (!lin_begin(args)) return;
     constexpr int SL = D2 / kSimtCols, ZR = D1 / 16;
-    int x = blockIdx.x;
-    const int slice = x % SL;
-    x /= SL;
-    const LinRole& role = args.role[x % args.roles];
-    x /= args.roles;
+    const int slice = x % args.slices;
+    x /= args.slices;
+    if (slice >= SL) return;                     // a role with fewer columns than another
+    const LinRole& role = args.role[ri];
     const int H = args.H, h = x % H, sidx = x / H;
     if (sidx >= args.map.segments()) return;
     const LinMap::Seg g = args.map.locate(sidx);
@@ -345,14 +344,28 @@ linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
     }
 }
 
-template <int D1, int D2>
+// One launch for all roles: those over (DK, DV) and those over (DV, DK).
+template <int DK, int DV>
+__global__ void __launch_bounds__(256, 1)
+linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
+{
+    if (!lin_begin(args)) return;
+    const int ri = blockIdx.x % args.roles, x = blockIdx.x / args.roles;
+    if (DK == DV || !args.role[ri].transposed) linear_simt_body<DK, DV>(args, ri, x, states_only);
+    else linear_simt_body<DV, DK>(args, ri, x, states_only);
+}
+
+template <int DK, int DV>
 cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
-    auto kern = linear_simt_kernel<D1, D2>;
-    const int smem = (int)sizeof(LinSimtSmem<D1>);
+    auto kern = linear_simt_kernel<DK, DV>;
+    const int smem = (int)std::max(sizeof(LinSimtSmem<DK>), sizeof(LinSimtSmem<DV>));
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const size_t grid = (size_t)a.max_segments * a.H * a.roles * (D2 / kSimtCols);
-    kern<<<(unsigned)grid, 256, smem, a.stream>>>(a, states_only ? 1 : 0);
+    LinArgs b = a;
+    b.slices = 1;
+    for (int i = 0; i < a.roles; ++i) b.slices = std::max(b.slices, a.dim[a.role[i].c] / kSimtCols);
+    const size_t grid = (size_t)a.max_segments * a.H * a.roles * b.slices;
+    kern<<<(unsigned)grid, 256, smem, a.stream>>>(b, states_only ? 1 : 0);
     return cudaGetLastError();
 }
 
@@ -370,13 +383,11 @@ cudaError_t launch_linear_scan(const LinArgs& a) {
     return cudaGetLastError();
 }
 
-// All roles of one launch have the same (D1, D2): those of its first role's inputs.
 cudaError_t launch_linear_simt(const LinArgs& a, bool states_only) {
-    const int d1 = a.dim[a.role[0].a], d2 = a.dim[a.role[0].c];
-    if (d1 == 128 && d2 == 128) return launch_simt_t<128, 128>(a, states_only);
-    if (d1 == 128 && d2 == 64) return launch_simt_t<128, 64>(a, states_only);
-    if (d1 == 64 && d2 == 128) return launch_simt_t<64, 128>(a, states_only);
-    if (d1 == 64 && d2 == 64) return launch_simt_t<64, 64>(a, states_only);
+    if (a.dk == 128 && a.dv == 128) return launch_simt_t<128, 128>(a, states_only);
+    if (a.dk == 128 && a.dv == 64) return launch_simt_t<128, 64>(a, states_only);
+    if (a.dk == 64 && a.dv == 128) return launch_simt_t<64, 128>(a, states_only);
+    if (a.dk == 64 && a.dv == 64) return launch_simt_t<64, 64>(a, states_only);
     return cudaErrorInvalidValue;
 }
 

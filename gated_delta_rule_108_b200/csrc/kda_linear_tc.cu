@@ -31,6 +31,8 @@
 // Every wait is bounded; one that gives up sets a flag that ends the CTA's other
 // waits, records KDA_ERR_TIMEOUT, and the CTA waits for its own copies and MMAs,
 // frees its TMEM and returns.
+#include <algorithm>
+
 #include "kda_linear.cuh"
 #include "kda_tc_common.cuh"
 
@@ -193,8 +195,7 @@ struct LinSmem {
 constexpr int kLinThreads = 19 * 32;
 
 template <int D1, int D2>
-__global__ void __launch_bounds__(kLinThreads, 1)
-linear_tc_kernel(const __grid_constant__ LinTcParams prm)
+__device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
 {
     using Sm = LinSmem<D1, D2>;
     extern __shared__ unsigned char smem_raw[];
@@ -209,11 +210,8 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
     __shared__ float diag[64], edge[32];
 
     const LinArgs& args = prm.a;
-    if (!lin_begin(args)) return;
-    int x = blockIdx.x;
-    const int ri = x % args.roles;
     const LinRole& role = args.role[ri];
-    x /= args.roles;
+    const int x = blockIdx.x / args.roles;
     const int H = args.H, h = x % H, sidx = x / H;
     if (sidx >= args.map.segments()) return;
     const LinMap::Seg g = args.map.locate(sidx);
@@ -557,6 +555,17 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
+// One launch for all roles: those over (DK, DV) and those over (DV, DK).
+template <int DK, int DV>
+__global__ void __launch_bounds__(kLinThreads, 1)
+linear_tc_kernel(const __grid_constant__ LinTcParams prm)
+{
+    if (!lin_begin(prm.a)) return;
+    const int ri = blockIdx.x % prm.a.roles;
+    if (DK == DV || !prm.a.role[ri].transposed) linear_tc_body<DK, DV>(prm, ri);
+    else linear_tc_body<DV, DK>(prm, ri);
+}
+
 // ----------------------------------------------------------- segment's sum --
 // Z of one segment from zero: sum_i lambda^{tokens from i to the segment's end}
 // b_i c_i^T.  The weights count to the segment's end, so nothing is rescaled.  Each
@@ -574,8 +583,7 @@ struct LinSumSmem {
 };
 
 template <int D1, int D2>
-__global__ void __launch_bounds__(320, 1)
-linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
+__device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int ri)
 {
     using Sm = LinSumSmem<D1, D2>;
     extern __shared__ unsigned char smem_raw[];
@@ -586,10 +594,8 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     __shared__ float pw[C + 1];
 
     const LinArgs& args = prm.a;
-    if (!lin_begin(args)) return;
-    int x = blockIdx.x;
-    const LinRole& role = args.role[x % args.roles];
-    x /= args.roles;
+    const LinRole& role = args.role[ri];
+    const int x = blockIdx.x / args.roles;
     const int H = args.H, h = x % H, sidx = x / H;
     if (sidx >= args.map.segments()) return;
     const LinMap::Seg g = args.map.locate(sidx);
@@ -722,11 +728,23 @@ linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
     if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
-template <int D1, int D2>
+template <int DK, int DV>
+__global__ void __launch_bounds__(320, 1)
+linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
+{
+    if (!lin_begin(prm.a)) return;
+    const int ri = blockIdx.x % prm.a.roles;
+    if (DK == DV || !prm.a.role[ri].transposed) linear_sum_tc_body<DK, DV>(prm, ri);
+    else linear_sum_tc_body<DV, DK>(prm, ri);
+}
+
+template <int DK, int DV>
 cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const LinArgs& a = p.a;
-    auto kern = states_only ? linear_sum_tc_kernel<D1, D2> : linear_tc_kernel<D1, D2>;
-    const int smem = (int)(states_only ? LinSumSmem<D1, D2>::END : LinSmem<D1, D2>::END) + 1024;
+    auto kern = states_only ? linear_sum_tc_kernel<DK, DV> : linear_tc_kernel<DK, DV>;
+    const uint32_t sum = std::max(LinSumSmem<DK, DV>::END, LinSumSmem<DV, DK>::END);
+    const uint32_t chunk = std::max(LinSmem<DK, DV>::END, LinSmem<DV, DK>::END);
+    const int smem = (int)(states_only ? sum : chunk) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? 320 : kLinThreads, smem, a.stream>>>(p);
@@ -756,11 +774,10 @@ cudaError_t launch_linear_tc(const LinArgs& a, bool states_only) {
         for (int i = 0; !states_only && i < a.roles; ++i)
             if (!encode(&p.ymap[i], a.role[i].y, a.dim[a.role[i].c])) return cudaErrorInvalidValue;
     }
-    const int d1 = a.dim[a.role[0].a], d2 = a.dim[a.role[0].c];   // the same for all roles of one launch
-    if (d1 == 128 && d2 == 128) return launch_tc_t<128, 128>(p, states_only);
-    if (d1 == 128 && d2 == 64) return launch_tc_t<128, 64>(p, states_only);
-    if (d1 == 64 && d2 == 128) return launch_tc_t<64, 128>(p, states_only);
-    if (d1 == 64 && d2 == 64) return launch_tc_t<64, 64>(p, states_only);
+    if (a.dk == 128 && a.dv == 128) return launch_tc_t<128, 128>(p, states_only);
+    if (a.dk == 128 && a.dv == 64) return launch_tc_t<128, 64>(p, states_only);
+    if (a.dk == 64 && a.dv == 128) return launch_tc_t<64, 128>(p, states_only);
+    if (a.dk == 64 && a.dv == 64) return launch_tc_t<64, 64>(p, states_only);
     return cudaErrorInvalidValue;
 }
 
