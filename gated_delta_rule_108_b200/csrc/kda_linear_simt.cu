@@ -129,17 +129,30 @@ linear_scan_kernel(const __grid_constant__ LinArgs a)
                             src[(size_t)(i + 2) * a.dv + j], src[(size_t)(i + 3) * a.dv + j]);
         }
     }
-    for (int n = 0; n < count; ++n) {
-        const int s = first + (role.reverse ? count - 1 - n : n);
-        float4* p = reinterpret_cast<float4*>(role.seg + ((size_t)s * a.H + h) * size + e);
-        float4 own = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n + 1 < count) own = *p;            // the last segment's own sum is not computed
-        *p = E;
-        const float w = lin_pow(l, a.map.locate(s).len);
-        E.x = fmaf(w, E.x, own.x);
-        E.y = fmaf(w, E.y, own.y);
-        E.z = fmaf(w, E.z, own.z);
-        E.w = fmaf(w, E.w, own.w);
+    // only a sequence's last segment may be short; it is the first one processed in reverse
+    const int tail = first + count - 1;
+    const float w_full = lin_pow(l, a.map.locate(first).len), w_tail = lin_pow(l, a.map.locate(tail).len);
+    constexpr int AHEAD = 8;                    // sums in flight
+    for (int n0 = 0; n0 < count; n0 += AHEAD) {
+        float4 own[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int n = n0 + k, s = role.reverse ? tail - n : first + n;
+            own[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n + 1 < count)                  // the last segment's own sum is not computed
+                own[k] = *reinterpret_cast<const float4*>(role.seg + ((size_t)s * a.H + h) * size + e);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int n = n0 + k, s = role.reverse ? tail - n : first + n;
+            if (n >= count) break;
+            *reinterpret_cast<float4*>(role.seg + ((size_t)s * a.H + h) * size + e) = E;
+            const float w = s == tail ? w_tail : w_full;
+            E.x = fmaf(w, E.x, own[k].x);
+            E.y = fmaf(w, E.y, own[k].y);
+            E.z = fmaf(w, E.z, own[k].z);
+            E.w = fmaf(w, E.w, own[k].w);
+        }
     }
 }
 

@@ -82,11 +82,11 @@ __device__ __forceinline__ void clear_rows(unsigned char* tile, int D, int L, in
     }
 }
 
-// 32 tokens of c from row i0 on, weighted, in `parts` bf16 parts of D2 / 64 tiles of
-// ROWS rows each, into rows r0.. of those; 256 threads, eight channels of each tile a
-// thread.  A row past L becomes zero.
+// Tokens of c from row i0 on, weighted, in `parts` bf16 parts of D2 / 64 tiles of ROWS
+// rows each; eight threads a row (32 rows with 256 threads), eight channels of each
+// tile a thread.  A row past L becomes zero.
 template <int D2, int ROWS>
-__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int i0, int r0, int parts, int L,
+__device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char* out, int i0, int parts, int L,
                                          const float* pw, float c_upd, bool rev, int t) {
     constexpr uint32_t PART = (D2 / 64) * ROWS * 128;
     const int i = i0 + (t >> 3);
@@ -96,7 +96,7 @@ __device__ __forceinline__ void weight_c(const unsigned char* ct, unsigned char*
 #pragma unroll
     for (int tile = 0; tile < D2 / 64; ++tile) raw[tile] = *reinterpret_cast<const uint4*>(ct + tile * kTile + src);
     const float w = on ? c_upd * pw[rev ? i + 1 : L - 1 - i] : 0.f;
-    out += sw128_offset(r0 + (t >> 3), (t & 7) * 16);
+    out += sw128_offset(t >> 3, (t & 7) * 16);
 #pragma unroll
     for (int tile = 0; tile < D2 / 64; ++tile) {
         if (!on) raw[tile] = make_uint4(0, 0, 0, 0);
@@ -433,7 +433,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
 
             // the update's last step, while P c runs
             if (!lin_wait_warp(&full_c[n & 1], (n >> 1) & 1, &s_abort) || !lin_wait_warp(&cw_free[1], 0, &s_abort)) break;
-            weight_c<D2, kLinStep>(buf_c(n), sm + Sm::Z, 3 * kLinStep, 0, parts, L, pw, c_upd, rev, tid);
+            weight_c<D2, kLinStep>(buf_c(n), sm + Sm::Z, 3 * kLinStep, parts, L, pw, c_upd, rev, tid);
             fence_proxy_async_smem();
             mbar_arrive(&cw_ready[1]);
 
@@ -526,7 +526,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
                 if (i == 2) ok = lin_wait_warp(&az_done, n & 1, &s_abort);
                 else if (n > 0 || i == 1) ok = lin_wait_warp(&cw_free[0], i == 0, &s_abort);
                 if (!ok) break;
-                weight_c<D2, kLinStep>(buf_c(n), sm + (i < 2 ? Sm::CW : Sm::Z), kLinStep * i, 0, parts, L, pw, c_upd, rev, t);
+                weight_c<D2, kLinStep>(buf_c(n), sm + (i < 2 ? Sm::CW : Sm::Z), kLinStep * i, parts, L, pw, c_upd, rev, t);
                 fence_proxy_async_smem();
                 mbar_arrive(&cw_ready[i >> 1]);
             }
@@ -569,9 +569,12 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 // ----------------------------------------------------------- segment's sum --
 // Z of one segment from zero: sum_i lambda^{tokens from i to the segment's end}
 // b_i c_i^T.  The weights count to the segment's end, so nothing is rescaled.  Each
-// chunk's sum is formed in TMEM (two of them, in turn) and added in registers, 64
+// chunk's sum is formed in TMEM (two of them, in turn) and added in registers, 32
 // elements a thread: the tensor core's cut-off sums would pile up over a long
-// segment.  Half a chunk of c is weighted while the other half is multiplied.
+// segment.  Half a chunk of c is weighted, by sixteen warps, while the other half is
+// multiplied.
+constexpr int kLinSumThreads = 18 * 32;
+
 template <int D1, int D2>
 struct LinSumSmem {
     static constexpr uint32_t BT = (D1 / 64) * kTile, CT = (D2 / 64) * kTile;
@@ -612,7 +615,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
         for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], 2);
             mbar_init(&empty[i], 1);
-            mbar_init(&cw_ready[i], 256);
+            mbar_init(&cw_ready[i], 512);
             mbar_init(&cw_free[i], 1);
         }
         mbar_init(&upd_done, 1);
@@ -630,7 +633,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     const uint32_t tmem = s_tmem;
     auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
 
-    if (warp == 9) {                                    // ---- TMA loads
+    if (warp == 17) {                                   // ---- TMA loads
         if (lane == 0) {
             int n = 0;
             for (; n < nch; ++n) {
@@ -644,7 +647,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
                 if (count > 0) (void)mbar_wait_cycles(&full[i], (count - 1) & 1, kWaitCycles);
             }
         }
-    } else if (warp == 8) {                             // ---- MMA issue
+    } else if (warp == 16) {                            // ---- MMA issue
         const uint64_t b_mn0 = smem_desc(smem_u32(sm), kTile, 1024, kLayoutSW128);
         const uint64_t w_mn0 = smem_desc(smem_u32(sm + Sm::CW), 64 * 128, 1024, kLayoutSW128);
         bool ok = true;
@@ -671,7 +674,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     } else {                                            // ---- weighted c, the sum
         const int quad = warp & 3, sub = warp >> 2, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-        constexpr int COLS = D2 / 2;                    // columns COLS sub .. of this thread's row
+        constexpr int COLS = D2 / 4;                    // columns COLS sub .. of this thread's row
         float z[COLS];
 #pragma unroll
         for (int j = 0; j < COLS; ++j) z[j] = 0.f;
@@ -680,11 +683,11 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
             tc_fence_after();
             if (D1 == 128 || quad < 2) {
 #pragma unroll
-                for (int j0 = 0; j0 < COLS; j0 += 32) {
-                    float v[32];
-                    tmem_ld32_sync(tmem + 128 * (n & 1) + lane_base + COLS * sub + j0, v);
+                for (int j0 = 0; j0 < COLS; j0 += 16) {
+                    float v[16];
+                    tmem_ld16_sync(tmem + 128 * (n & 1) + lane_base + COLS * sub + j0, v);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j0 + j] += v[j];
+                    for (int j = 0; j < 16; ++j) z[j0 + j] += v[j];
                 }
             }
             tc_fence_before();
@@ -699,7 +702,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
             ok = lin_wait_warp(&full[n & 1], (n >> 1) & 1, &s_abort);
             if (!ok) break;
             if (L < C) {
-                clear_rows(bt, D1, L, 0, C, tid, 256);
+                clear_rows(bt, D1, L, 0, C, tid, 512);
                 fence_proxy_async_smem();
             }
 #pragma unroll 1
@@ -707,9 +710,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
                 // the last chunk's sum before this chunk's second half, without which the barrier cannot go on
                 if (n > 0) ok = lin_wait_warp(&cw_free[half], (n - 1) & 1, &s_abort) && (half == 0 || add(n - 1));
                 if (!ok) break;
-#pragma unroll
-                for (int r = 0; r < 64; r += 32)
-                    weight_c<D2, 64>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, 64 * half + r, r, parts, L, pw, cw, rev, tid);
+                weight_c<D2, 64>(bt + Sm::BT, sm + Sm::CW + half * Sm::CWH, 64 * half, parts, L, pw, cw, rev, tid);
                 fence_proxy_async_smem();
                 mbar_arrive(&cw_ready[half]);
             }
@@ -729,7 +730,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
 }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kLinSumThreads, 1)
 linear_sum_tc_kernel(const __grid_constant__ LinTcParams prm)
 {
     if (!lin_begin(prm.a)) return;
@@ -747,7 +748,7 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const int smem = (int)(states_only ? sum : chunk) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? 320 : kLinThreads, smem, a.stream>>>(p);
+    kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? kLinSumThreads : kLinThreads, smem, a.stream>>>(p);
     return cudaGetLastError();
 }
 

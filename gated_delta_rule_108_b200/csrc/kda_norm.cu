@@ -267,22 +267,24 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
 }
 
 // dw of one side, 32 channels per CTA: the CTAs' partial sums in a fixed order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 norm_weight_grad_kernel(const float* __restrict__ partial, int ctas, int d, float* dwq, float* dwk)
 {
-    __shared__ double red[8][33];
+    __shared__ double red[32][33];
     const int q = blockIdx.y, lane = threadIdx.x & 31, part = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float* dw = q ? dwk : dwq;
     if (!dw) return;
     double v = 0.0;
-    if (i < d)
-        for (int n = part; n < ctas; n += 8) v += (double)partial[((size_t)n * 2 + q) * d + i];
+    if (i < d) {
+#pragma unroll 4
+        for (int n = part; n < ctas; n += 32) v += (double)partial[((size_t)n * 2 + q) * d + i];
+    }
     red[part][lane] = v;
     __syncthreads();
-    if (part == 0 && i < d) {
-        for (int k = 1; k < 8; ++k) v += red[k][lane];
-        dw[i] = (float)v;
-    }
+    v = red[lane][part];                       // this warp's channel, one part a lane
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0 && blockIdx.x * 32 + part < d) dw[blockIdx.x * 32 + part] = (float)v;
 }
 
 template <typename T, bool BWD, bool INTER>
@@ -367,7 +369,7 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
             : launch_norm<float>(a, bwd, interleaved != 0, ctas, static_cast<cudaStream_t>(stream));
     }
     if (e == cudaSuccess && sums) {
-        norm_weight_grad_kernel<<<dim3((d + 31) / 32, 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        norm_weight_grad_kernel<<<dim3((d + 31) / 32, 2), 1024, 0, static_cast<cudaStream_t>(stream)>>>(
             a.partial, ctas, d, dwq, dwk);
         e = cudaGetLastError();
     }
