@@ -129,6 +129,16 @@ __device__ __forceinline__ double lin_log_decay(const float* log_decay, int h) {
 }
 __device__ __forceinline__ float lin_pow(double l, int n) { return (float)exp(l * (double)n); }
 
+// How many of a segment's chunks, in processing order, add nothing to the state that
+// leaves it: those after which so many tokens follow that the decay over them is zero
+// in fp32 (e^-104 is below half the smallest number).
+__device__ __forceinline__ int lin_skip(double l, int len, int chunk, int chunks, bool rev) {
+    if (l > -1e-7) return 0;                       // no decay that 2^30 tokens could bring to zero
+    const double reach = 104.0 / -l;               // tokens
+    if (reach >= (double)len) return 0;
+    return rev ? max(chunks - 1 - (int)(reach / chunk), 0) : max((len - (int)reach - 1) / chunk, 0);
+}
+
 cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens);
 cudaError_t launch_linear_scan(const LinArgs& a);
 cudaError_t launch_linear_simt(const LinArgs& a, bool states_only);

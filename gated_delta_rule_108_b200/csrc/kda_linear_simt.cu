@@ -209,8 +209,9 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
     const float* pb = static_cast<const float*>(args.x[role.b]);
     const float* pc = static_cast<const float*>(args.x[role.c]);
     float* py = static_cast<float*>(role.y);
-    const int nch = (g.len + kSimtChunk - 1) / kSimtChunk;
-    auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
+    const int chunks = (g.len + kSimtChunk - 1) / kSimtChunk;
+    const int skip = states_only ? lin_skip(l, g.len, kSimtChunk, chunks, rev) : 0, nch = chunks - skip;
+    auto chunk_of = [&](int n) { return rev ? nch - 1 - n : skip + n; };
     auto fetch = [&](int n) {                    // chunk n's tiles on their way
         if (n < nch) {
             typename Sm::Tile& t = sm.tile[n & 1];

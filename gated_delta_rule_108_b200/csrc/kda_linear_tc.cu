@@ -604,11 +604,11 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     const LinMap::Seg g = args.map.locate(sidx);
     const bool rev = role.reverse;
     if (g.index == (rev ? 0 : g.count - 1)) return;     // processed last: its sum enters no other segment
-    const int nch = (g.len + C - 1) / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = role.s_out ? 3 : 2;
     const float c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
+    const int chunks = (g.len + C - 1) / C, skip = lin_skip(l, g.len, C, chunks, rev), nch = chunks - skip;
 
     if (tid == 0) {
         s_abort = 0;
@@ -631,7 +631,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    auto chunk_of = [&](int n) { return rev ? nch - 1 - n : n; };
+    auto chunk_of = [&](int n) { return rev ? nch - 1 - n : skip + n; };
 
     if (warp == 17) {                                   // ---- TMA loads
         if (lane == 0) {
