@@ -302,6 +302,20 @@ cudaError_t launch_norm(const NormArgs& a, bool bwd, bool interleaved, int ctas,
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Bytes [lo, hi) that a tensor's elements lie in.
+struct Extent { const char* lo; const char* hi; };
+Extent dense(const void* p, int64_t bytes) { return {static_cast<const char*>(p), static_cast<const char*>(p) + bytes}; }
+Extent strided(const void* p, const int64_t* s, int B, int T, int H, int d, int es) {
+    const int64_t n[3] = {B, T, H};
+    int64_t lo = 0, hi = d;
+    for (int i = 0; i < 3; ++i) (s[i] < 0 ? lo : hi) += s[i] * (n[i] - 1);
+    return {static_cast<const char*>(p) + lo * es, static_cast<const char*>(p) + hi * es};
+}
+bool is_dense(const int64_t* s, int B, int T, int H, int d) {
+    return (H == 1 || s[2] == d) && (T == 1 || s[1] == (int64_t)H * d) && (B == 1 || s[0] == (int64_t)T * H * d);
+}
+bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+
 size_t partial_bytes(int d) { return sizeof(float) * 2 * (size_t)d * kMaxCtas; }
 
 kda_status check_sizes(int B, int T, int Hq, int Hk, int d, int rot, kda_dtype dtype, kda_norm norm, float eps) {
@@ -336,6 +350,18 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
         for (int i = 0; i < 3; ++i)
             if (qs[i] % per16 || ks[i] % per16)
                 return (kda_status)set_error(KDA_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+        // an output may be its own input, contiguous: each row is read before it is written
+        const int es = dtype == KDA_BF16 ? 2 : 4;
+        const Extent xq = strided(q, qs, B, T, Hq, d, es), xk = strided(k, ks, B, T, Hk, d, es);
+        const Extent yq = dense(oq, tokens * Hq * d * es), yk = dense(ok_, tokens * Hk * d * es);
+        const bool own_q = !bwd && oq == q && is_dense(qs, B, T, Hq, d), own_k = !bwd && ok_ == k && is_dense(ks, B, T, Hk, d);
+        if ((!own_q && meet(yq, xq)) || (!own_k && meet(yk, xk)) || meet(yq, xk) || meet(yk, xq) || meet(yq, yk))
+            return (kda_status)set_error(KDA_ERR_INVALID_ARG, "an output overlaps an input or the other output");
+        if (bwd) {
+            const Extent gq = dense(dyq, tokens * Hq * d * es), gk = dense(dyk, tokens * Hk * d * es);
+            if (meet(yq, gq) || meet(yq, gk) || meet(yk, gq) || meet(yk, gk))
+                return (kda_status)set_error(KDA_ERR_INVALID_ARG, "an output overlaps a cotangent");
+        }
     }
     if (sums) {
         if (!workspace || workspace_bytes < partial_bytes(d))
