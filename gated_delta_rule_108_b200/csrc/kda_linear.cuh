@@ -26,13 +26,14 @@ namespace kda {
 
 constexpr int kLinChunk = 128;    // tokens per chunk: the rows of one tensor-core tile
 constexpr int kLinMaxRoles = 3;
+constexpr int kLinDirect = 8;     // segments per sequence up to which no scan is launched
 
 struct LinRole {
     int a, b, c;            // LinArgs::x indices of the query-, key- and value-like inputs
     void* y;                // output [tokens, H, D2], input dtype
     const float* s_in;      // state before the first processed token, nullable (zeros)
     float* s_out;           // state after the last one, nullable
-    float* seg;             // [segments][H][D1 * D2]: each segment's own sum, then its entering state
+    float* seg;             // [segments][H][D1 * D2]: each segment's own sum; after the scan its entering state
     bool transposed;        // Z is the transpose of the user's [dk, dv] states
     bool reverse;           // from the last token to the first
     float c_inter, c_intra; // y_t = c_inter lambda^.. Z_0^T a_t + c_intra sum_i lambda^.. <a_t, b_i> c_i
@@ -45,7 +46,8 @@ struct LinRole {
 // sequence a single pass over the tokens does all; otherwise a pass over keys and
 // values first sums every segment's own contribution to the state, and a scan
 // turns those into the states that enter each segment, so that all segments run
-// at the same time.
+// at the same time.  With few segments (kLinDirect) each CTA forms its entering state
+// from the sums of the segments before it, and there is no scan.
 // Packed sequences: tab = [seg_tok][first segment of the r-th sequence, r = 0..N]
 // [r-th sequence], longest first, so that long segments start first.
 struct LinMap {
@@ -57,6 +59,7 @@ struct LinMap {
     struct Seg {
         int seq, begin, len;      // sequence, first token in the flat token order, tokens
         int index, count;         // which segment of how many of its sequence
+        int size, tail;           // tokens of each of them, and of the last one
     };
     __device__ __forceinline__ int segments() const { return cu ? tab[1 + N] : N * num_seg; }
     __device__ __forceinline__ void range(int r, int& seq, int& first, int& count) const {   // r-th sequence's segments
@@ -86,6 +89,8 @@ struct LinMap {
         const int off = g.index * size;          // < seq_len + size, see the host's check of T
         g.begin = seq_begin + off;
         g.len = min(size, seq_len - off);
+        g.size = size;
+        g.tail = seq_len - (g.count - 1) * size;
         return g;
     }
 };
@@ -100,6 +105,7 @@ struct LinArgs {
     LinMap map;
     int max_segments;             // host bound on map.segments()
     bool split;                   // some sequence may have more than one segment
+    bool scanned;                 // and the scan has turned sums into entering states
     int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role
     LinRole role[kLinMaxRoles];
     WsHeader* hdr;
@@ -128,6 +134,18 @@ __device__ __forceinline__ double lin_log_decay(const float* log_decay, int h) {
     return l < -1e30f ? -1e30 : (double)l;
 }
 __device__ __forceinline__ float lin_pow(double l, int n) { return (float)exp(l * (double)n); }
+
+// The sums before segment g of a sequence, in processing order: `fold(slot, w)` is to
+// make E = w E + (the sum in that slot), E beginning as the initial state.
+template <class Fold>
+__device__ __forceinline__ void lin_enter(const LinMap::Seg& g, int sidx, bool rev, double l, Fold fold) {
+    const int first = sidx - g.index, n = rev ? g.count - 1 - g.index : g.index;
+    const float w_full = lin_pow(l, g.size), w_tail = lin_pow(l, g.tail);
+    for (int i = 0; i < n; ++i) {
+        const int at = rev ? g.count - 1 - i : i;
+        fold(first + at, at == g.count - 1 ? w_tail : w_full);
+    }
+}
 
 // How many of a segment's chunks, in processing order, add nothing to the state that
 // leaves it: those after which so many tokens follow that the decay over them is zero

@@ -135,7 +135,11 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     if (p.split && e == cudaSuccess) {
         e = pass(true);
         all.reset = false;
-        if (e == cudaSuccess) e = launch_linear_scan(all);
+        // the most segments a sequence may have; and a state updated in place is read by the
+        // scan, before the chunk kernel's last segments overwrite it
+        all.scanned = (all.map.cu ? all.map.T / p.seg_tok + 1 : p.num_seg) > kLinDirect;
+        for (int i = 0; i < all.roles; ++i) all.scanned |= all.role[i].s_in && all.role[i].s_in == all.role[i].s_out;
+        if (e == cudaSuccess && all.scanned) e = launch_linear_scan(all);
     }
     return e == cudaSuccess ? pass(false) : e;
 }

@@ -232,8 +232,9 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
     fetch(0);
 
     float2 z[ZR][2];
-    const float* from = states_only ? nullptr : (g.count > 1 ? seg : (role.s_in ? role.s_in + user : nullptr));
-    const bool tr_in = g.count == 1 && role.transposed;
+    const bool scanned = args.scanned && g.count > 1;
+    const float* from = states_only ? nullptr : (scanned ? seg : (role.s_in ? role.s_in + user : nullptr));
+    const bool tr_in = !scanned && role.transposed;
 #pragma unroll
     for (int n = 0; n < ZR; ++n) {
         const int i = ty * ZR + n, j = j0 + 4 * tx;
@@ -245,6 +246,16 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
         z[n][0] = make_float2(v.x, v.y);
         z[n][1] = make_float2(v.z, v.w);
     }
+    if (!states_only && !scanned)
+        lin_enter(g, sidx, rev, l, [&](int slot, float w) {
+            const float* own = role.seg + ((size_t)slot * H + h) * zsize + (size_t)ty * ZR * D2 + j0 + 4 * tx;
+#pragma unroll
+            for (int n = 0; n < ZR; ++n) {
+                const float4 u = *reinterpret_cast<const float4*>(own + (size_t)n * D2);
+                z[n][0] = fma2(make_float2(w, w), z[n][0], make_float2(u.x, u.y));
+                z[n][1] = fma2(make_float2(w, w), z[n][1], make_float2(u.z, u.w));
+            }
+        });
     for (int n = 0; n < nch; ++n) {
         const int ch = chunk_of(n);
         const int tok0 = g.begin + ch * kSimtChunk, L = min(kSimtChunk, g.len - ch * kSimtChunk);

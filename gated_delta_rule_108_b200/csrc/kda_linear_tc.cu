@@ -469,12 +469,20 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
         bool ok = true;
         const bool mine = D1 == 128 || quad < 2;        // warps with rows of Z
         if (mine) {
-            const float* from = g.count > 1 ? role.seg + ((size_t)sidx * H + h) * zsize
-                                            : (role.s_in ? role.s_in + user : nullptr);
+            const bool scanned = args.scanned && g.count > 1;
+            const float* from = scanned ? role.seg + ((size_t)sidx * H + h) * zsize : (role.s_in ? role.s_in + user : nullptr);
+            const double l = lin_log_decay(args.log_decay, h);
 #pragma unroll 1
             for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
-                read_state<D1, D2>(from, g.count == 1 && role.transposed, row, j0, v);
+                read_state<D1, D2>(from, !scanned && role.transposed, row, j0, v);
+                if (!scanned)
+                    lin_enter(g, sidx, rev, l, [&](int slot, float w) {
+                        float u[32];
+                        read_state<D1, D2>(role.seg + ((size_t)slot * H + h) * zsize, false, row, j0, u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = fmaf(w, v[j], u[j]);
+                    });
                 tmem_st32_sync(ZREG + lane_base + j0, v);
             }
         }

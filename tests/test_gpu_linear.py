@@ -99,7 +99,7 @@ def test_forward_packed(cuda_device, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
-@pytest.mark.parametrize("B,T,lens", [(1, 3001, None), (2, 1500, None), (1, 3100, (2900, 0, 1, 199)), (1, 4000, (1300, 1350, 1350))],
+@pytest.mark.parametrize("B,T,lens", [(1, 700, None), (2, 333, None), (1, 600, (600, 0)), (1, 3001, None), (2, 1500, None), (1, 3100, (2900, 0, 1, 199)), (1, 4000, (1300, 1350, 1350))],
                          ids=str)
 def test_segments(cuda_device, B, T, lens, dtype):
     """Few heads and long sequences: cut into segments (a packed batch by its longest sequence)."""
@@ -179,7 +179,7 @@ def test_other_sequences_do_not_leak(cuda_device, dtype):
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 def test_state_in_place_and_repeat(cuda_device, dtype):
     """final_state may be initial_state itself; the same call gives the same bits."""
-    for T in (200, 3000):      # one segment, several
+    for T in (200, 700, 3000):      # one segment, a few, many
         x, back = case(1, T, 1, 128, 128, dtype, seed=11)
         x, back = dev(x), dev(back)
         o, S = kda.linear_chunk_fwd(**x)
