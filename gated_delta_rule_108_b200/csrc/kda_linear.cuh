@@ -48,6 +48,9 @@ struct LinRole {
 // turns those into the states that enter each segment, so that all segments run
 // at the same time.  With few segments (kLinDirect) each CTA forms its entering state
 // from the sums of the segments before it, and there is no scan.
+// Or the segments of a sequence run one after another, each starting from the state
+// that the one before has left in memory (LinArgs::chained): nothing is summed twice,
+// and chains that do not divide evenly among the SMs still do.
 // Packed sequences: tab = [seg_tok][first segment of the r-th sequence, r = 0..N]
 // [r-th sequence], longest first, so that long segments start first.
 struct LinMap {
@@ -106,6 +109,8 @@ struct LinArgs {
     int max_segments;             // host bound on map.segments()
     bool split;                   // some sequence may have more than one segment
     bool scanned;                 // and the scan has turned sums into entering states
+    bool chained;                 // segments take their entering state from the one before
+    int* flags;                   // chained: [segments][H][roles] warps that have left their part of the state
     int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role
     LinRole role[kLinMaxRoles];
     WsHeader* hdr;

@@ -22,19 +22,36 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool supported_dim(int d) { return d == 64 || d == 128; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Into how many segments a sequence of `chunks` chunks is cut, when `chains`
-// CTAs work on each segment number: the cheapest by the count of waves.  In units
-// of one chunk of the chunk kernel, a chunk of the summing pass costs 0.55, a CTA
-// 0.8 to start and end, and the two extra launches 2.5 together.
-int plan_segment_chunks(int64_t chains, int64_t chunks) {
-    if (chunks <= 1) return 1;
-    double best = 0;
-    int64_t best_len = chunks;
+// How long the segments of a sequence of `chunks` chunks are, when `chains` CTAs work
+// on each segment number: the cheapest by the count of waves over the SMs.  In units
+// of one chunk of the chunk kernel (3.8 us at dk = dv = 128), as measured: a chunk of
+// the summing pass 0.5, a CTA 1.5 to start and end (1 there), its launch 2.
+int plan_segment_chunks(int64_t chains, int64_t chunks, double& best) {
+    int64_t best_len = std::max<int64_t>(chunks, 1);
+    best = 0;
     for (int64_t s = 1; s <= std::min<int64_t>(chunks, 96); ++s) {
         const int64_t len = (chunks + s - 1) / s, n = (chunks + len - 1) / len;
         const double waves = std::ceil((double)(chains * n) / kSms), sums = std::ceil((double)(chains * (n - 1)) / kSms);
-        const double cost = waves * (len + 0.8) + (n > 1 ? sums * (0.55 * len + 0.8) + 2.5 : 0.0);
+        const double cost = waves * (len + 1.5) + (n > 1 ? sums * (0.5 * len + 1.0) + 2.0 : 0.0);
         if (s == 1 || cost < best) {
+            best = cost;
+            best_len = len;
+        }
+    }
+    return (int)best_len;
+}
+
+// The same where segments follow one another: n of them take n turns at least; 2.5 for
+// a segment's start and end with the state handed on, 1 for clearing the flags.  The
+// gradients at B=4, T=4096, H=16 (192 chains of 32 chunks): 248 us uncut, 210 in two,
+// 209 in three, 253 in four segments.
+int plan_chained_chunks(int64_t chains, int64_t chunks, double& best) {
+    int64_t best_len = 0;
+    for (int64_t s = 2; s <= std::min<int64_t>(chunks, 16); ++s) {
+        const int64_t len = (chunks + s - 1) / s, n = (chunks + len - 1) / len;
+        const double turns = std::max(std::ceil((double)(chains * n) / kSms), (double)n);
+        const double cost = turns * (len + 2.5) + 1.0;
+        if (best_len == 0 || cost < best) {
             best = cost;
             best_len = len;
         }
@@ -44,8 +61,9 @@ int plan_segment_chunks(int64_t chains, int64_t chunks) {
 
 struct Plan {
     int N, seg_tok, num_seg, max_segments, balance_tokens;
-    bool split;
+    bool split, chained;
     size_t tab_off, seg_off, seg_bytes, total;   // seg_bytes: one role's segment states
+    size_t flag_bytes;                           // chained: the flags, where packed batches have their table
 };
 
 bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, kda_dtype dtype, int roles, Plan& p) {
@@ -58,10 +76,14 @@ bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, k
     const int64_t per_head = (int64_t)roles * (dtype == KDA_BF16 ? 1 : std::max(dk, dv) / 64);
     const int64_t chunks = ((int64_t)T + kLinChunk - 1) / kLinChunk;
     const int64_t chains = per_head * H * (varlen ? 1 : std::max(B, 1));
-    const int len = plan_segment_chunks(chains, chunks);
+    double cost = 0, cost_chained = 0;
+    int len = plan_segment_chunks(chains, chunks, cost);
+    const int len_chained = (varlen || dtype != KDA_BF16) ? 0 : plan_chained_chunks(chains, chunks, cost_chained);
+    p.chained = len_chained > 0 && cost_chained < 0.95 * cost;
+    if (p.chained) len = len_chained;
     p.seg_tok = std::max(len, 1) * kLinChunk;
     p.num_seg = std::max<int>(1, (int)((chunks + len - 1) / std::max(len, 1)));
-    p.split = p.num_seg > 1;
+    p.split = p.num_seg > 1 && !p.chained;
     // packed: every sequence may end in a short segment; unsplit when the longest
     // is within 1.6 times one SM's share (the summing pass would cost 0.6 of it)
     const int64_t most = varlen ? (int64_t)p.N + T / p.seg_tok : (int64_t)p.N * p.num_seg;
@@ -70,8 +92,9 @@ bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, k
     p.balance_tokens = (int)std::min<int64_t>((int64_t)1 << 30, (int64_t)(1.6 * (double)T * H * per_head / kSms));
     if (!p.split) p.balance_tokens = 1 << 30;
     p.tab_off = kHeaderBytes;
-    p.seg_off = round_up(p.tab_off + (varlen ? sizeof(int32_t) * (2 * (size_t)p.N + 2) : 0), 256);
-    p.seg_bytes = p.split ? sizeof(float) * (size_t)p.max_segments * H * dk * dv : 0;
+    p.flag_bytes = p.chained ? sizeof(int) * (size_t)p.max_segments * H * roles : 0;
+    p.seg_off = round_up(p.tab_off + (varlen ? sizeof(int32_t) * (2 * (size_t)p.N + 2) : p.flag_bytes), 256);
+    p.seg_bytes = p.split || p.chained ? sizeof(float) * (size_t)p.max_segments * H * dk * dv : 0;
     p.total = round_up(p.seg_off + p.seg_bytes * roles, 256);
     return true;
 }
@@ -125,11 +148,17 @@ LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, in
 cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     LinArgs all = a;
     for (int i = 0; i < all.roles; ++i)
-        all.role[i].seg = p.split ? reinterpret_cast<float*>(ws + p.seg_off + p.seg_bytes * i) : nullptr;
+        all.role[i].seg = p.split || p.chained ? reinterpret_cast<float*>(ws + p.seg_off + p.seg_bytes * i) : nullptr;
     cudaError_t e = cudaSuccess;
     if (all.map.cu) e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
     else if (p.max_segments == 0) e = cudaMemsetAsync(all.hdr, 0, sizeof(WsHeader), all.stream);
     if (p.max_segments == 0) return e;
+    if (p.chained) {
+        all.chained = true;
+        all.flags = reinterpret_cast<int*>(ws + p.tab_off);
+        e = cudaMemsetAsync(ws, 0, p.tab_off + p.flag_bytes, all.stream);   // status, claims and flags
+        return e == cudaSuccess ? launch_linear_tc(all, false) : e;
+    }
     auto pass = [&](bool states_only) { return all.bf16 ? launch_linear_tc(all, states_only) : launch_linear_simt(all, states_only); };
     all.reset = true;
     if (p.split && e == cudaSuccess) {

@@ -152,10 +152,10 @@ __device__ __forceinline__ void read_state(const float* s, bool transposed, int 
     } else if (transposed) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = s[(size_t)(j0 + j) * D1 + i];
-    } else {
+    } else {            // past L1: another block of this launch may have written it
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(s + (size_t)i * D2 + j0 + j);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(s + (size_t)i * D2 + j0 + j));
             v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
         }
     }
@@ -170,6 +170,31 @@ __device__ __forceinline__ void write_state(float* s, bool transposed, int i, in
         for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(s + (size_t)i * D2 + j0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
+}
+
+// A state handed from one block to a later one: each warp counts itself in once its
+// part is written; every warp of the reader waits for all of them.
+__device__ __forceinline__ void raise_flag(int* flag) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence();
+        atomicAdd(flag, 1);
+    }
+}
+__device__ __forceinline__ bool wait_flag(const int* flag, int count, int* s_abort) {
+    const long long t0 = clock64();
+    int seen;
+    do {
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+        if (seen < count) {
+            if (*(volatile int*)s_abort || clock64() - t0 > kWaitCycles) {
+                *(volatile int*)s_abort = 1;
+                break;
+            }
+            __nanosleep(200);
+        }
+    } while (seen < count);
+    return __all_sync(0xffffffffu, seen >= count);
 }
 
 // ------------------------------------------------------------- chunk kernel --
@@ -195,7 +220,7 @@ struct LinSmem {
 constexpr int kLinThreads = 19 * 32;
 
 template <int D1, int D2>
-__device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
+__device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, int x)
 {
     using Sm = LinSmem<D1, D2>;
     extern __shared__ unsigned char smem_raw[];
@@ -211,7 +236,6 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
 
     const LinArgs& args = prm.a;
     const LinRole& role = args.role[ri];
-    const int x = blockIdx.x / args.roles;
     const int H = args.H, h = x % H, sidx = x / H;
     if (sidx >= args.map.segments()) return;
     const LinMap::Seg g = args.map.locate(sidx);
@@ -470,13 +494,16 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
         const bool mine = D1 == 128 || quad < 2;        // warps with rows of Z
         if (mine) {
             const bool scanned = args.scanned && g.count > 1;
-            const float* from = scanned ? role.seg + ((size_t)sidx * H + h) * zsize : (role.s_in ? role.s_in + user : nullptr);
+            const int before = sidx + (rev ? 1 : -1);           // the segment processed before this one
+            const bool chained = args.chained && g.index != (rev ? g.count - 1 : 0);
+            if (chained) ok = wait_flag(args.flags + ((size_t)before * H + h) * args.roles + ri, D1 / 16, &s_abort);
+            const float* from = chained ? role.seg + ((size_t)before * H + h) * zsize : scanned ? role.seg + ((size_t)sidx * H + h) * zsize : (role.s_in ? role.s_in + user : nullptr);
             const double l = lin_log_decay(args.log_decay, h);
 #pragma unroll 1
             for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
-                read_state<D1, D2>(from, !scanned && role.transposed, row, j0, v);
-                if (!scanned)
+                read_state<D1, D2>(from, !scanned && !chained && role.transposed, row, j0, v);
+                if (!scanned && !args.chained)
                     lin_enter(g, sidx, rev, l, [&](int slot, float w) {
                         float u[32];
                         read_state<D1, D2>(role.seg + ((size_t)slot * H + h) * zsize, false, row, j0, u);
@@ -540,8 +567,10 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
             }
         }
         if (ok && nch > 0) ok = lin_wait_warp(&upd_done, (nch - 1) & 1, &s_abort);
-        if (ok && mine && role.s_out && g.index == (rev ? 0 : g.count - 1)) {
+        const bool last = g.index == (rev ? 0 : g.count - 1), hand = args.chained && !last;
+        if (ok && mine && (hand || (last && role.s_out))) {
             tc_fence_after();
+            float* to = hand ? role.seg + ((size_t)sidx * H + h) * zsize : role.s_out + user;
             const float gam = nch > 0 ? pw[min(C, g.len - chunk_of(nch - 1) * C)] : 1.f;
 #pragma unroll 1
             for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
@@ -553,8 +582,9 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = fmaf(gam, v[j], u[j]);
                 }
-                write_state<D1, D2>(role.s_out + user, role.transposed, row, j0, v);
+                write_state<D1, D2>(to, !hand && role.transposed, row, j0, v);
             }
+            if (hand) raise_flag(args.flags + ((size_t)sidx * H + h) * args.roles + ri);
         }
     }
     tc_fence_before();
@@ -568,10 +598,23 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(kLinThreads, 1)
 linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 {
-    if (!lin_begin(prm.a)) return;
-    const int ri = blockIdx.x % prm.a.roles;
-    if (DK == DV || !prm.a.role[ri].transposed) linear_tc_body<DK, DV>(prm, ri);
-    else linear_tc_body<DV, DK>(prm, ri);
+    const LinArgs& a = prm.a;
+    if (!lin_begin(a)) return;
+    int ri = blockIdx.x % a.roles, x = blockIdx.x / a.roles;
+    if (a.chained) {
+        // Work is claimed in order, all first segments before all second ones: the state a
+        // segment waits for comes from work that was claimed before and is running or done,
+        // in whatever order the blocks have started.
+        __shared__ int claimed;
+        if (threadIdx.x == 0) claimed = atomicAdd(&a.hdr->next_pair, 1);
+        __syncthreads();
+        const int chains = a.map.N * a.H * a.roles, j = claimed / chains, c = claimed - j * chains;
+        ri = c % a.roles;
+        const int nh = c / a.roles, n = nh / a.H, h = nh - n * a.H;
+        x = (n * a.map.num_seg + (a.role[ri].reverse ? a.map.num_seg - 1 - j : j)) * a.H + h;
+    }
+    if (DK == DV || !a.role[ri].transposed) linear_tc_body<DK, DV>(prm, ri, x);
+    else linear_tc_body<DV, DK>(prm, ri, x);
 }
 
 // ----------------------------------------------------------- segment's sum --

@@ -133,6 +133,25 @@ def test_backward_packed(cuda_device, decay, dtype):
     check_bwd(x, back, full)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("T", [2000, 2048])
+def test_more_chains_than_sms(cuda_device, T, dk, dv):
+    """160 and 480 chains of 16 chunks: segments that follow one another, each from the state of the one before."""
+    x, back = case(5, T, 32, dk, dv, torch.bfloat16, seed=T + dk)
+    for _ in range(3):          # the flags of the last call do not count
+        o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+        g = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
+    S0 = x["initial_state"].cuda()
+    o2, S2 = kda.linear_chunk_fwd(**{**dev(x), "initial_state": S0}, final_state=S0)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    for b, h in ((0, 0), (2, 13), (4, 31)):
+        one = {n: t[b:b + 1, :, h:h + 1] for n, t in x.items() if n in "qkv"}
+        one.update(log_decay=x["log_decay"][h:h + 1], initial_state=x["initial_state"][b:b + 1, h:h + 1], cu_seqlens=None)
+        ob = dict(d_o=back["d_o"][b:b + 1, :, h:h + 1], d_final_state=back["d_final_state"][b:b + 1, h:h + 1])
+        check_fwd(one, o[b:b + 1, :, h:h + 1], S[b:b + 1, h:h + 1])
+        check_bwd(one, ob, {n: (t[b:b + 1, h:h + 1] if n == "dS0" else t[b:b + 1, :, h:h + 1]) for n, t in g.items()})
+
+
 def test_backward_against_differences(cuda_device):
     """L is linear in each input alone, so a step of any size changes it by <gradient, step>."""
     x, back = case(1, 200, 2, 64, 64, torch.float32, seed=9)
