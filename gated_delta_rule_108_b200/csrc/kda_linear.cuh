@@ -114,6 +114,7 @@ struct LinArgs {
     int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role
     LinRole role[kLinMaxRoles];
     WsHeader* hdr;
+    long long wait_cap;           // test hook: cycles after which a wait gives up, one copy left out (0: neither)
     bool reset;                   // the launch starts the call: block 0 clears the status
     cudaStream_t stream;
 };

@@ -11,6 +11,8 @@
 namespace kda {
 namespace {
 
+thread_local long long g_drop_cap = 0;   // armed by kda_linear_debug_drop_copy (one call)
+
 constexpr int kSms = 148;   // the plan and the workspace size are those of one B200
 
 template <typename... A>
@@ -219,9 +221,19 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
     for (int i = 0; i < 4; ++i) { a.x[i] = x[i]; a.dim[i] = dims[i]; }
     const float s = 1.0f / sqrtf((float)dk);
     a.roles = 1;
+    if (a.bf16) {
+        a.wait_cap = g_drop_cap;
+        g_drop_cap = 0;
+    }
     a.role[0] = {0, 1, 2, o, initial_state, final_state, nullptr, false, false, s, s, 1.f};
     const cudaError_t e = run_roles(a, p, static_cast<char*>(workspace));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_chunk_fwd launch failed: %s", cudaGetErrorString(e));
+    return fail(KDA_OK, "");
+}
+
+kda_status kda_linear_debug_drop_copy(long long wait_cycles) {
+    if (wait_cycles < 0) return fail(KDA_ERR_INVALID_ARG, "wait_cycles=%lld < 0", wait_cycles);
+    g_drop_cap = wait_cycles;
     return fail(KDA_OK, "");
 }
 

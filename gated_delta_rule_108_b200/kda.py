@@ -101,6 +101,8 @@ def _declare(lib):
     lib.kda_set_stage_events.argtypes = [ctypes.POINTER(vp), i]
     lib.kda_debug_drop_copy.restype = i
     lib.kda_debug_drop_copy.argtypes = [ctypes.c_longlong]
+    lib.kda_linear_debug_drop_copy.restype = i
+    lib.kda_linear_debug_drop_copy.argtypes = [ctypes.c_longlong]
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
     lib.kda_version.restype = ctypes.c_char_p
@@ -620,6 +622,12 @@ def linear_recurrent_step(q, k, v, log_decay, state, o=None, stream=None) -> tor
     if status != KDA_OK:
         _check(status)
     return o
+
+
+def linear_debug_drop_copy(wait_cycles: int) -> None:
+    """Arm the one-shot failure-path test hook of the next bf16 :func:`linear_chunk_fwd`
+    (``kda_linear_debug_drop_copy``)."""
+    _check(lib().kda_linear_debug_drop_copy(int(wait_cycles)))
 
 
 # ------------------------------------------------ norm and rotation of q and k --

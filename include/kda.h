@@ -483,6 +483,14 @@ kda_status kda_set_stage_events(void* const* events, int count);
  */
 kda_status kda_debug_drop_copy(long long wait_cycles);
 
+/*
+ * The same for the next kda_linear_chunk_fwd with bf16 inputs on this host thread
+ * (one call only): its chunk kernel's first block leaves out the query tile of its
+ * third chunk (of its last one, if it has fewer) and every wait of the call is
+ * capped at `wait_cycles` cycles.  0 disarms.
+ */
+kda_status kda_linear_debug_drop_copy(long long wait_cycles);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char* kda_last_error(void);
 

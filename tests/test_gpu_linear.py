@@ -1,5 +1,7 @@
 """Linear attention with one fixed decay per head on the GPU: the chunked forward,
 its gradients and the single-token step against the fp64 recurrence."""
+import time
+
 import pytest
 import torch
 
@@ -306,3 +308,20 @@ def test_training_shape_sampled(cuda_device):
         ob = dict(d_o=back["d_o"][b:b + 1, :, h:h + 1], d_final_state=back["d_final_state"][b:b + 1, h:h + 1])
         check_fwd(one, o[b:b + 1, :, h:h + 1], S[b:b + 1, h:h + 1])
         check_bwd(one, ob, {n: (t[b:b + 1, h:h + 1] if n == "dS0" else t[b:b + 1, :, h:h + 1]) for n, t in g.items()})
+
+
+@pytest.mark.parametrize("B,T,H", [(1, 100, 2), (3, 380, 50), (5, 2048, 32)])
+def test_missing_copy_reports_timeout_then_recovers(cuda_device, B, T, H):
+    """A wait that can never end gives up: one chunk, several, segments that wait for one another."""
+    x, _ = case(B, T, H, 128, 64, torch.bfloat16, seed=18)
+    d = dev(x)
+    ws = torch.empty(kda.linear_chunk_fwd_workspace_size(B, T, H, 128, 64, B, False, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    o, S = kda.linear_chunk_fwd(**d, workspace=ws)
+    assert kda.workspace_status(ws) == 0
+    kda.linear_debug_drop_copy(4_000_000)     # about 2 ms
+    t0 = time.perf_counter()
+    kda.linear_chunk_fwd(**d, workspace=ws)
+    assert kda.workspace_status(ws) == 4      # KDA_ERR_TIMEOUT
+    assert time.perf_counter() - t0 < 1.0
+    o2, S2 = kda.linear_chunk_fwd(**d, workspace=ws, check=True)
+    assert torch.equal(o, o2) and torch.equal(S, S2)

@@ -141,6 +141,11 @@ def test_step_refuses(lib, over, status):
     assert lib.kda_last_error()
 
 
+def test_hook_arms_and_disarms(lib):
+    assert lib.kda_linear_debug_drop_copy(-1) == 1
+    assert lib.kda_linear_debug_drop_copy(1000) == 0 and lib.kda_linear_debug_drop_copy(0) == 0
+
+
 NORM_BAD = [(dict(d=12), 2), (dict(d=264), 2), (dict(rot=24), 2), (dict(rot=80), 2), (dict(dtype=2), 1), (dict(norm=2), 1),
             (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(Hk=0), 1), (dict(q=None), 1),
             (dict(k=OK_PTR + 8), 1), (dict(qs=(64, 64, 62)), 1), (dict(freq=None), 1), (dict(wq=OK_PTR + 4), 1),
