@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -113,7 +115,7 @@ struct LinArgs {
     int* flags;                   // chained: [segments][H][roles] warps that have left their part of the state
     int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role
     LinRole role[kLinMaxRoles];
-    WsHeader* hdr;
+    WsHeader* hdr;                // null where a call needs no more workspace than this and the caller gave none
     long long wait_cap;           // test hook: cycles after which a wait gives up, one copy left out (0: neither)
     bool reset;                   // the launch starts the call: block 0 clears the status
     cudaStream_t stream;
@@ -125,7 +127,7 @@ struct LinArgs {
 // error only after a wait of a second).
 __device__ __forceinline__ bool lin_begin(const LinArgs& a) {
     if (a.map.cu) return a.hdr->status == kStatusOk;
-    if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) {
+    if (a.reset && a.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
         a.hdr->status = kStatusOk;
         a.hdr->runtime_err = 0;
     }
@@ -161,6 +163,19 @@ __device__ __forceinline__ int lin_skip(double l, int len, int chunk, int chunks
     const double reach = 104.0 / -l;               // tokens
     if (reach >= (double)len) return 0;
     return rev ? max(chunks - 1 - (int)(reach / chunk), 0) : max((len - (int)reach - 1) / chunk, 0);
+}
+
+// Allows a kernel its shared memory on the current device, once: `done` holds a bit
+// for each device (above 64 it is set at every call).
+inline cudaError_t lin_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens);

@@ -115,6 +115,7 @@ kda_status check_sizes(int B, int T, int H, int dk, int dv, int num_seqs, bool v
 }
 
 kda_status check_workspace(void* workspace, size_t bytes, size_t need) {
+    if (!workspace && need <= (size_t)kHeaderBytes) return KDA_OK;   // nothing but the status would be in it
     if (!workspace) return fail(KDA_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
@@ -153,7 +154,7 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
         all.role[i].seg = p.split || p.chained ? reinterpret_cast<float*>(ws + p.seg_off + p.seg_bytes * i) : nullptr;
     cudaError_t e = cudaSuccess;
     if (all.map.cu) e = launch_linear_prep(all, const_cast<int32_t*>(all.map.tab), p.seg_tok, p.balance_tokens);
-    else if (p.max_segments == 0) e = cudaMemsetAsync(all.hdr, 0, sizeof(WsHeader), all.stream);
+    else if (p.max_segments == 0 && all.hdr) e = cudaMemsetAsync(all.hdr, 0, sizeof(WsHeader), all.stream);
     if (p.max_segments == 0) return e;
     if (p.chained) {
         all.chained = true;

@@ -384,7 +384,8 @@ template <int DK, int DV>
 cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
     auto kern = linear_simt_kernel<DK, DV>;
     const int smem = (int)std::max(sizeof(LinSimtSmem<DK>), sizeof(LinSimtSmem<DV>));
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = lin_allow_smem(reinterpret_cast<const void*>(kern), smem, done);
     if (e != cudaSuccess) return e;
     LinArgs b = a;
     b.slices = 1;

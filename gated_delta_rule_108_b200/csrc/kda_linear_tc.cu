@@ -598,7 +598,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && s_wait.abort) flag_error(args.hdr, kStatusTimeout);
+    if (tid == 0 && s_wait.abort && args.hdr) flag_error(args.hdr, kStatusTimeout);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -786,7 +786,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && s_wait.abort) flag_error(args.hdr, kStatusTimeout);
+    if (tid == 0 && s_wait.abort && args.hdr) flag_error(args.hdr, kStatusTimeout);
     if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
@@ -807,7 +807,8 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const uint32_t sum = std::max(LinSumSmem<DK, DV>::END, LinSumSmem<DV, DK>::END);
     const uint32_t chunk = std::max(LinSmem<DK, DV>::END, LinSmem<DV, DK>::END);
     const int smem = (int)(states_only ? sum : chunk) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t e = lin_allow_smem(reinterpret_cast<const void*>(kern), smem, done[states_only]);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? kLinSumThreads : kLinThreads, smem, a.stream>>>(p);
     return cudaGetLastError();

@@ -342,7 +342,7 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     const int64_t tokens = (int64_t)B * T;
     const bool sums = bwd && (dwq || dwk);
     if (tokens > 0) {
-        if (!q || !k || !oq || !ok_ || !qs || !ks || (bwd && (!dyq || !dyk)) || (rot && !inv_freq))
+        if (!q || !k || !oq || !ok_ || (bwd && (!dyq || !dyk)) || (rot && !inv_freq))
             return (kda_status)set_error(KDA_ERR_INVALID_ARG, "null pointer");
         const int per16 = dtype == KDA_BF16 ? 8 : 4;
         if (!aligned16(q) || !aligned16(k) || !aligned16(oq) || !aligned16(ok_) || !aligned16(wq) || !aligned16(wk) || (bwd && (!aligned16(dyq) || !aligned16(dyk))))
@@ -373,8 +373,8 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     NormArgs a{};
-    a.side[0] = {q, dyq, oq, wq, qs ? qs[0] : 0, qs ? qs[1] : 0, qs ? qs[2] : 0, Hq};
-    a.side[1] = {k, dyk, ok_, wk, ks ? ks[0] : 0, ks ? ks[1] : 0, ks ? ks[2] : 0, Hk};
+    a.side[0] = {q, dyq, oq, wq, qs[0], qs[1], qs[2], Hq};
+    a.side[1] = {k, dyk, ok_, wk, ks[0], ks[1], ks[2], Hk};
     a.inv_freq = inv_freq; a.positions = positions;
     a.T = T > 0 ? T : 1; a.d = d; a.rot = rot; a.tokens = tokens;
     a.m = norm == KDA_NORM_RMS ? 1.f / (float)d : 1.f;
@@ -410,8 +410,10 @@ extern "C" {
 
 kda_status kda_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
                             const float* inv_freq, const int32_t* positions, int B, int T, int Hq, int Hk, int d,
-                            int rotary_dim, const int64_t* q_strides, const int64_t* k_strides, kda_dtype dtype,
+                            int rotary_dim, int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_b,
+                            int64_t k_stride_t, int64_t k_stride_h, kda_dtype dtype,
                             kda_norm norm, float eps, int interleaved, void* q_out, void* k_out, void* stream) {
+    const int64_t q_strides[3] = {q_stride_b, q_stride_t, q_stride_h}, k_strides[3] = {k_stride_b, k_stride_t, k_stride_h};
     return kda::run_norm(q, k, nullptr, nullptr, q_weight, k_weight, inv_freq, positions, B, T, Hq, Hk, d, rotary_dim,
                          q_strides, k_strides, dtype, norm, eps, interleaved, q_out, k_out, nullptr, nullptr, nullptr, 0,
                          stream, false);
@@ -424,9 +426,11 @@ size_t kda_qk_norm_rope_bwd_workspace_size(int d) {
 kda_status kda_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const void* d_k_out,
                                 const float* q_weight, const float* k_weight, const float* inv_freq,
                                 const int32_t* positions, int B, int T, int Hq, int Hk, int d, int rotary_dim,
-                                const int64_t* q_strides, const int64_t* k_strides, kda_dtype dtype, kda_norm norm,
+                                int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_b,
+                            int64_t k_stride_t, int64_t k_stride_h, kda_dtype dtype, kda_norm norm,
                                 float eps, int interleaved, void* dq, void* dk, float* dq_weight, float* dk_weight,
                                 void* workspace, size_t workspace_bytes, void* stream) {
+    const int64_t q_strides[3] = {q_stride_b, q_stride_t, q_stride_h}, k_strides[3] = {k_stride_b, k_stride_t, k_stride_h};
     return kda::run_norm(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, positions, B, T, Hq, Hk, d, rotary_dim,
                          q_strides, k_strides, dtype, norm, eps, interleaved, dq, dk, dq_weight, dk_weight, workspace,
                          workspace_bytes, stream, true);

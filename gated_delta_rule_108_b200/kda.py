@@ -87,14 +87,13 @@ def _declare(lib):
                                          vp, vp, vp, vp, vp, sz, vp]
     lib.kda_linear_recurrent_step.restype = i
     lib.kda_linear_recurrent_step.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
-    ip = ctypes.POINTER(ctypes.c_int64)
+    ll = ctypes.c_int64
     lib.kda_qk_norm_rope.restype = i
-    lib.kda_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ip, ip, i, i, f, i, vp, vp, vp]
+    lib.kda_qk_norm_rope.argtypes = [vp] * 6 + [i] * 6 + [ll] * 6 + [i, i, f, i, vp, vp, vp]
     lib.kda_qk_norm_rope_bwd_workspace_size.restype = sz
     lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [i]
     lib.kda_qk_norm_rope_bwd.restype = i
-    lib.kda_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ip, ip, i, i, f, i,
-                                         vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 6 + [ll] * 6 + [i, i, f, i, vp, vp, vp, vp, vp, sz, vp]
     lib.kda_workspace_status.restype = i
     lib.kda_workspace_status.argtypes = [vp, sz, vp]
     lib.kda_set_stage_events.restype = i
@@ -492,10 +491,14 @@ def _verify(device, specs) -> None:
             _need(t, name, dtype, device)
 
 
-def _run_status(status: int, workspace, stream, device, check: Optional[bool]) -> None:
+def _workspace_args(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+
+
+def _run_status(status: int, workspace, stream, device, check: bool) -> None:
     if status != KDA_OK:
         _check(status)
-    if check if check is not None else _validate_default():
+    if check:
         _check_device_status(workspace, stream if stream is not None else torch.cuda.current_stream(device))
 
 
@@ -535,24 +538,26 @@ def linear_chunk_fwd(q, k, v, log_decay=None, initial_state=None, cu_seqlens=Non
                   (cu_seqlens, "cu_seqlens", None, torch.int32), (o, "o", (B, T, H, dv), dtype),
                   (final_state, "final_state", state, f32), (workspace, "workspace", None, None)))
     code = _dtype_code(q)
+    check = _validate_default() if check is None else check
     made = []
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=dtype, device=dev)
+        o = torch.empty_like(v)
         made.append(o)
     if final_state is None and output_final_state:
-        final_state = torch.empty(state, dtype=f32, device=dev)
+        final_state = torch.empty(state, dtype=f32, device=dev) if initial_state is None else torch.empty_like(initial_state)
         made.append(final_state)
     if workspace is None:
         size = _loaded().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, code)
-        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        if check or size != 256:        # 256: the status alone, which nobody would read
+            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+            made.append(workspace)
     if stream is not None:
         _used_on(stream, dev, *made)
     with _on(dev):
         status = _loaded().kda_linear_chunk_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(log_decay), _addr(initial_state), _addr(cu_seqlens),
             B, T, H, dk, dv, N, code, o.data_ptr(), _addr(final_state),
-            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+            *_workspace_args(workspace), _raw_stream(stream, dev))
         _run_status(status, workspace, stream, dev, check)
     return o, final_state
 
@@ -577,20 +582,22 @@ def linear_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=
                   (initial_state, "initial_state", state, f32), (d_final_state, "d_final_state", state, f32),
                   (cu_seqlens, "cu_seqlens", None, torch.int32), (workspace, "workspace", None, None)))
     code = _dtype_code(q)
+    check = _validate_default() if check is None else check
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
          "dS0": torch.empty(state, dtype=f32, device=dev) if output_d_initial_state else None}
     made = list(g.values())
     if workspace is None:
         size = _loaded().kda_linear_chunk_bwd_workspace_size(B, T, H, dk, dv, N, cu_seqlens is not None, code)
-        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        if check or size != 256:        # 256: the status alone, which nobody would read
+            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+            made.append(workspace)
     if stream is not None:
         _used_on(stream, dev, *made)
     with _on(dev):
         status = _loaded().kda_linear_chunk_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(log_decay), _addr(initial_state), _addr(cu_seqlens),
             d_o.data_ptr(), _addr(d_final_state), B, T, H, dk, dv, N, code, g["dq"].data_ptr(), g["dk"].data_ptr(),
-            g["dv"].data_ptr(), _addr(g["dS0"]), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+            g["dv"].data_ptr(), _addr(g["dS0"]), *_workspace_args(workspace), _raw_stream(stream, dev))
         _run_status(status, workspace, stream, dev, check)
     return g
 
@@ -612,7 +619,7 @@ def linear_recurrent_step(q, k, v, log_decay, state, o=None, stream=None) -> tor
                   (o, "o", (B, H, dv), dtype)))
     code = _dtype_code(q)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=dtype, device=dev)
+        o = torch.empty_like(v)
         if stream is not None:
             _used_on(stream, dev, o)
     with _on(dev):
@@ -631,9 +638,6 @@ def linear_debug_drop_copy(wait_cycles: int) -> None:
 
 
 # ------------------------------------------------ norm and rotation of q and k --
-_INT64x3 = ctypes.c_int64 * 3
-
-
 def _rows(t: torch.Tensor, name: str, dtype, device):
     """Element strides of batch, token and head of rows that may lie apart: only
     their channels are contiguous."""
@@ -645,15 +649,13 @@ def _rows(t: torch.Tensor, name: str, dtype, device):
     if s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
     # a dimension of one element is never stepped over, whatever stride torch gives it
-    head = s[-2] if n[-2] != 1 else 0
-    first = s[0] if n[0] != 1 else 0
-    return _INT64x3(first, s[1] if len(n) == 4 and n[1] != 1 else 0, head)
+    return (s[0] if n[0] != 1 else 0, s[1] if len(n) == 4 and n[1] != 1 else 0, s[-2] if n[-2] != 1 else 0)
 
 
 def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm, more):
-    """Checks the arguments the norm and its gradients share; returns the sizes
-    (B, T, Hq, Hk, d, rotary_dim), the norm's code and the strides.  ``more`` names
-    the tensors shaped like q and like k."""
+    """Checks the arguments the norm and its gradients share; returns the sizes and
+    strides as the C calls take them and the norm's code.  ``more`` names the tensors
+    shaped like q and like k."""
     ndim = q.dim()
     if ndim not in (3, 4):
         raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(q.shape)}")
@@ -676,7 +678,7 @@ def _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm, more):
     _verify(dev, ((q_weight, "q_weight", (d,), f32), (k_weight, "k_weight", (d,), f32),
                   (inv_freq, "inv_freq", None, f32), (positions, "positions", lead, torch.int32),
                   *[(t, n, qshape if of_q else kshape, dtype) for t, n, of_q in more]))
-    return (B, T, Hq, Hk, d, rot), code, _rows(q, "q", dtype, dev), _rows(k, "k", dtype, dev)
+    return (B, T, Hq, Hk, d, rot, *_rows(q, "q", dtype, dev), *_rows(k, "k", dtype, dev)), code
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, norm: str = "l2",
@@ -693,22 +695,22 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
     [B, T] ([B] for single tokens), None: 0 .. T-1.  Returns (q_out, k_out),
     contiguous and of the inputs' dtype.
     """
-    sizes, code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
-                                     ((q_out, "q_out", True), (k_out, "k_out", False)))
+    sizes, code = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
+                             ((q_out, "q_out", True), (k_out, "k_out", False)))
     dev, dt = q.device, _dtype_code(q)
     made = []
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         made.append(q_out)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         made.append(k_out)
     if stream is not None:
         _used_on(stream, dev, *made)
     with _on(dev):
         status = _loaded().kda_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), *sizes,
-            qs, ks, dt, code, eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(stream, dev))
+            dt, code, eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), _raw_stream(stream, dev))
     if status != KDA_OK:
         _check(status)
     return q_out, k_out
@@ -720,10 +722,11 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, inv_f
     """Gradients of :func:`qk_norm_rope` (``kda_qk_norm_rope_bwd``): q, k its inputs,
     d_q_out, d_k_out the cotangents of its outputs.  Returns a dict with dq, dk
     (contiguous) and dq_weight, dk_weight [d] fp32 (None without that weight)."""
-    sizes, code, qs, ks = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
-                                     ((d_q_out, "d_q_out", True), (d_k_out, "d_k_out", False)))
+    sizes, code = _norm_args(q, k, q_weight, k_weight, inv_freq, positions, norm,
+                             ((d_q_out, "d_q_out", True), (d_k_out, "d_k_out", False)))
     dev, dt = q.device, _dtype_code(q)
-    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+    g = {"dq": torch.empty_like(q, memory_format=torch.contiguous_format),
+         "dk": torch.empty_like(k, memory_format=torch.contiguous_format),
          "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
          "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
     made = list(g.values())
@@ -737,7 +740,7 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, inv_f
     with _on(dev):
         status = _loaded().kda_qk_norm_rope_bwd(
             q.data_ptr(), k.data_ptr(), d_q_out.data_ptr(), d_k_out.data_ptr(), _addr(q_weight), _addr(k_weight),
-            _addr(inv_freq), _addr(positions), *sizes, qs, ks, dt, code, eps, interleaved, g["dq"].data_ptr(),
+            _addr(inv_freq), _addr(positions), *sizes, dt, code, eps, interleaved, g["dq"].data_ptr(),
             g["dk"].data_ptr(), _addr(g["dq_weight"]), _addr(g["dk_weight"]), _addr(workspace),
             0 if workspace is None else workspace.nbytes, _raw_stream(stream, dev))
     if status != KDA_OK:

@@ -344,7 +344,8 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
  *              may be empty: their final state is their initial state); o must
  *              not overlap an input
  *  workspace   at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
- *              aligned; its contents on entry do not matter.  Calls that share
+ *              aligned; its contents on entry do not matter.  Where the size is 256,
+ *              the status alone, NULL is allowed: then the call has no status.  Calls that share
  *              one workspace must be ordered on one stream.
  *              kda_workspace_status reads its status (KDA_ERR_BAD_SEQLENS,
  *              KDA_ERR_TIMEOUT).
@@ -414,8 +415,8 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
  * normed.  The angle is formed in fp64.
  *
  *  q           [B, T, Hq, d], k [B, T, Hk, d]: dtype, 16-byte aligned, the channels
- *              of a head contiguous; q_strides / k_strides are the element strides
- *              of batch, token and head (host arrays, multiples of 16 bytes), so a
+ *              of a head contiguous; q_stride_b, _t, _h (and k_stride_..) are the
+ *              element strides of batch, token and head (multiples of 16 bytes), so a
  *              slice of a joint projection is taken as it lies
  *  q_weight, k_weight [d] fp32, 16-byte aligned, or NULL for ones
  *  inv_freq    [rotary_dim / 2] fp32 (NULL only with rotary_dim = 0)
@@ -429,8 +430,9 @@ typedef enum { KDA_NORM_RMS = 0, KDA_NORM_L2 = 1 } kda_norm;
 kda_status kda_qk_norm_rope(const void* q, const void* k, const float* q_weight,
                             const float* k_weight, const float* inv_freq,
                             const int32_t* positions, int B, int T, int Hq, int Hk, int d,
-                            int rotary_dim, const int64_t* q_strides, const int64_t* k_strides,
-                            kda_dtype dtype, kda_norm norm, float eps, int interleaved,
+                            int rotary_dim, int64_t q_stride_b, int64_t q_stride_t,
+                            int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_t,
+                            int64_t k_stride_h, kda_dtype dtype, kda_norm norm, float eps, int interleaved,
                             void* q_out, void* k_out, void* stream);
 
 /*
@@ -446,8 +448,9 @@ kda_status kda_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_ou
                                 const void* d_k_out, const float* q_weight,
                                 const float* k_weight, const float* inv_freq,
                                 const int32_t* positions, int B, int T, int Hq, int Hk, int d,
-                                int rotary_dim, const int64_t* q_strides,
-                                const int64_t* k_strides, kda_dtype dtype, kda_norm norm,
+                                int rotary_dim, int64_t q_stride_b, int64_t q_stride_t,
+                                int64_t q_stride_h, int64_t k_stride_b, int64_t k_stride_t,
+                                int64_t k_stride_h, kda_dtype dtype, kda_norm norm,
                                 float eps, int interleaved, void* dq, void* dk,
                                 float* dq_weight, float* dk_weight, void* workspace,
                                 size_t workspace_bytes, void* stream);

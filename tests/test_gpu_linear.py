@@ -212,6 +212,18 @@ def test_state_in_place_and_repeat(cuda_device, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_without_a_workspace(cuda_device, dtype):
+    """Where the workspace holds nothing but the status, there may be none."""
+    for T in (0, 100):
+        x, back = case(2, T, 2, 128, 64, dtype, seed=19)
+        assert kda.linear_chunk_fwd_workspace_size(2, T, 2, 128, 64, 2, False, dtype) == 256
+        a, b = (kda.linear_chunk_fwd(**dev(x), check=c) for c in (False, True))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        a, b = (kda.linear_chunk_bwd(**dev(x), **dev(back), check=c) for c in (False, True))
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 def test_no_tokens(cuda_device, dtype):
     x, back = case(2, 0, 2, 128, 64, dtype, seed=12)
     o, S = kda.linear_chunk_fwd(**dev(x), check=True)

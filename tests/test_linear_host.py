@@ -1,8 +1,6 @@
 """Linear attention with one decay per head and the query/key norm, without a GPU:
 the fp64 plain forms against closed forms and differences, the workspace sizes, and
 every refusal of the C entry points and of the binding (nothing is launched)."""
-import ctypes
-
 import pytest
 import torch
 
@@ -106,7 +104,7 @@ def fwd(lib, **over):
 
 
 BAD = [(dict(dk=96), 2), (dict(dv=32), 2), (dict(dtype=7), 1), (dict(q=None), 1), (dict(k=OK_PTR + 4), 1), (dict(H=0), 1),
-       (dict(B=-1), 1), (dict(B=2, cu=OK_PTR), 1), (dict(cu=OK_PTR, N=-1), 1), (dict(ws=None), 5), (dict(ws=OK_PTR + 16), 5),
+       (dict(B=-1), 1), (dict(B=2, cu=OK_PTR), 1), (dict(cu=OK_PTR, N=-1), 1), (dict(ws=None, T=6000, dtype=1), 5), (dict(ws=None, cu=OK_PTR), 5), (dict(ws=OK_PTR + 16), 5),
        (dict(wsb=16), 5), (dict(T=1 << 30), 2), (dict(H=70000), 2)]
 
 
@@ -157,8 +155,7 @@ def norm_call(lib, bwd, **over):
              d=64, rot=64, qs=(192, 64, 64), ks=(192, 64, 64), dtype=0, norm=0, eps=1e-6, oq=3 * OK_PTR, ok=4 * OK_PTR,
              dwq=None, dwk=None, ws=None, wsb=0)
     a.update(over)
-    arr = lambda t: (ctypes.c_int64 * 3)(*t)  # noqa: E731
-    common = (a["wq"], a["wk"], a["freq"], a["pos"], a["B"], a["T"], a["Hq"], a["Hk"], a["d"], a["rot"], arr(a["qs"]), arr(a["ks"]),
+    common = (a["wq"], a["wk"], a["freq"], a["pos"], a["B"], a["T"], a["Hq"], a["Hk"], a["d"], a["rot"], *a["qs"], *a["ks"],
               a["dtype"], a["norm"], a["eps"], 0, a["oq"], a["ok"])
     if not bwd:
         return lib.kda_qk_norm_rope(a["q"], a["k"], *common, None)
