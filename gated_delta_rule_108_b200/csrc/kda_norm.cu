@@ -26,6 +26,7 @@
 #include "../../include/kda.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace kda {
 namespace {
@@ -37,8 +38,8 @@ struct NormSide {
     const void* x; const void* dy;     // dy: backward only
     void* out;                         // y, or dx
     const float* w;                    // [d], nullable
-    int64_t sb, st, sh;                // element strides of x (batch, token, head)
-    int heads;
+    int64_t sb, st;                    // element strides of x (batch, token)
+    int sh, heads;                     // and head
 };
 struct NormArgs {
     NormSide side[2];                  // queries, keys
@@ -53,6 +54,7 @@ struct NormArgs {
 template <typename T> struct Vec4;
 template <> struct Vec4<__nv_bfloat16> {
     uint2 raw;
+    __device__ __forceinline__ void zero() { raw = make_uint2(0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = __ldcs(reinterpret_cast<const uint2*>(p)); }
     __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = unpack_bf16(raw.x); x[1] = unpack_bf16(raw.y); }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&x)[2]) {
@@ -61,6 +63,7 @@ template <> struct Vec4<__nv_bfloat16> {
 };
 template <> struct Vec4<float> {
     float4 raw;
+    __device__ __forceinline__ void zero() { raw = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) { raw = __ldcs(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = make_float2(raw.x, raw.y); x[1] = make_float2(raw.z, raw.w); }
     static __device__ __forceinline__ void store(float* p, const float2 (&x)[2]) {
@@ -131,9 +134,10 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
             const int shift = q ? a.side[0].heads : 0;
             const int lo = max(first - shift, 0), hi = min(end - shift, z.heads);    // this unit's heads of this side
             if (lo >= hi) continue;
-            const T* x_tok = static_cast<const T*>(z.x) + b * z.sb + t * z.st;
-            const T* g_tok = BWD ? static_cast<const T*>(z.dy) + tok * z.heads * (int64_t)a.d : nullptr;
-            T* out_tok = static_cast<T*>(z.out) + tok * z.heads * (int64_t)a.d;
+            const T* x_tok = static_cast<const T*>(z.x) + b * z.sb + t * z.st + e0;
+            const T* g_tok = BWD ? static_cast<const T*>(z.dy) + tok * z.heads * (int64_t)a.d + e0 : nullptr;
+            T* out_tok = static_cast<T*>(z.out) + tok * z.heads * (int64_t)a.d + e0;
+            const int sh = z.sh, to1 = e1 - e0;
             // y = n c + (other of n's pair) s, with c and s times the weights in the forward
             float2 w[4], c[4], s[4];
 #pragma unroll
@@ -166,14 +170,20 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
 #pragma unroll
                 for (int n = 0; n < kUnroll; ++n) {     // all loads first
                     const int r = r0 + n * RPW + sub;
+                    xv[n][0].zero();
+                    xv[n][1].zero();
+                    if constexpr (BWD) {
+                        gv[n][0].zero();
+                        gv[n][1].zero();
+                    }
                     if (r < hi && mine) {
-                        const T* p = x_tok + r * z.sh;
-                        xv[n][0].load(p + e0);
-                        xv[n][1].load(p + e1);
+                        const T* p = x_tok + r * sh;
+                        xv[n][0].load(p);
+                        xv[n][1].load(p + to1);
                         if constexpr (BWD) {
-                            const T* g = g_tok + r * (int64_t)a.d;
-                            gv[n][0].load(g + e0);
-                            gv[n][1].load(g + e1);
+                            const T* g = g_tok + r * a.d;
+                            gv[n][0].load(g);
+                            gv[n][1].load(g + to1);
                         }
                     }
                 }
@@ -181,15 +191,9 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
                 for (int n = 0; n < kUnroll; ++n) {
                     if (r0 + n * RPW >= hi) break;      // uniform over the warp
                     const int r = r0 + n * RPW + sub;
-                    const bool on = r < hi && mine;
                     float2 x[4], h[4];
-                    if (on) {
-                        xv[n][0].get(*reinterpret_cast<float2(*)[2]>(&x[0]));
-                        xv[n][1].get(*reinterpret_cast<float2(*)[2]>(&x[2]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = make_float2(0.f, 0.f);
-                    }
+                    xv[n][0].get(*reinterpret_cast<float2(*)[2]>(&x[0]));
+                    xv[n][1].get(*reinterpret_cast<float2(*)[2]>(&x[2]));
                     float2 ss = mul2(x[0], x[0]);
 #pragma unroll
                     for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
@@ -204,13 +208,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
                         }
                     } else {
                         float2 g[4], dot = make_float2(0.f, 0.f);
-                        if (on) {
-                            gv[n][0].get(*reinterpret_cast<float2(*)[2]>(&g[0]));
-                            gv[n][1].get(*reinterpret_cast<float2(*)[2]>(&g[2]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) g[i] = make_float2(0.f, 0.f);
-                        }
+                        gv[n][0].get(*reinterpret_cast<float2(*)[2]>(&g[0]));
+                        gv[n][1].get(*reinterpret_cast<float2(*)[2]>(&g[2]));
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float2 y = mul2(g[i], c[i]);
@@ -226,10 +225,10 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) h[i] = mul2(rr, fma2(make_float2(k, k), x[i], h[i]));
                     }
-                    if (on) {
-                        T* out = out_tok + r * (int64_t)a.d;
-                        Vec4<T>::store(out + e0, *reinterpret_cast<const float2(*)[2]>(&h[0]));
-                        Vec4<T>::store(out + e1, *reinterpret_cast<const float2(*)[2]>(&h[2]));
+                    if (r < hi && mine) {
+                        T* out = out_tok + r * a.d;
+                        Vec4<T>::store(out, *reinterpret_cast<const float2(*)[2]>(&h[0]));
+                        Vec4<T>::store(out + to1, *reinterpret_cast<const float2(*)[2]>(&h[2]));
                     }
                 }
             }
@@ -350,6 +349,9 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
         for (int i = 0; i < 3; ++i)
             if (qs[i] % per16 || ks[i] % per16)
                 return (kda_status)set_error(KDA_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+        const int64_t reach = (int64_t)1 << 31;   // of a token's heads, whose offsets are 32 bits
+        if (std::abs(qs[2]) * Hq >= reach || std::abs(ks[2]) * Hk >= reach || (int64_t)std::max(Hq, Hk) * d >= reach)
+            return (kda_status)set_error(KDA_ERR_UNSUPPORTED, "the heads of one token span 2^31 elements or more");
         // an output may be its own input, contiguous: each row is read before it is written
         const int es = dtype == KDA_BF16 ? 2 : 4;
         const Extent xq = strided(q, qs, B, T, Hq, d, es), xk = strided(k, ks, B, T, Hk, d, es);
@@ -373,8 +375,8 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     NormArgs a{};
-    a.side[0] = {q, dyq, oq, wq, qs[0], qs[1], qs[2], Hq};
-    a.side[1] = {k, dyk, ok_, wk, ks[0], ks[1], ks[2], Hk};
+    a.side[0] = {q, dyq, oq, wq, qs[0], qs[1], (int)qs[2], Hq};
+    a.side[1] = {k, dyk, ok_, wk, ks[0], ks[1], (int)ks[2], Hk};
     a.inv_freq = inv_freq; a.positions = positions;
     a.T = T > 0 ? T : 1; a.d = d; a.rot = rot; a.tokens = tokens;
     a.m = norm == KDA_NORM_RMS ? 1.f / (float)d : 1.f;
