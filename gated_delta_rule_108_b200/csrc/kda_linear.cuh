@@ -161,21 +161,29 @@ __device__ __forceinline__ void lin_enter(const LinMap::Seg& g, int sidx, bool r
 __device__ __forceinline__ int lin_skip(double l, int len, int chunk, int chunks, bool rev) {
     if (l > -1e-7) return 0;                       // no decay that 2^30 tokens could bring to zero
     const double reach = 104.0 / -l;               // tokens
-    if (reach >= (double)len) return 0;
+    if (!(reach < (double)len)) return 0;         // a NaN among the decays skips nothing
     return rev ? max(chunks - 1 - (int)(reach / chunk), 0) : max((len - (int)reach - 1) / chunk, 0);
 }
 
-// Allows a kernel its shared memory on the current device, once: `done` holds a bit
-// for each device (above 64 it is set at every call).
-inline cudaError_t lin_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+// Launches a kernel with more shared memory than every kernel may have.  It is allowed
+// that on the current device once (`done` holds a bit for each device, above 64 every
+// call asks), and again if this launch itself is refused, as after a reset of the
+// device; an error that an earlier call has left says nothing about this one.
+inline cudaError_t lin_launch(const void* kernel, size_t grid, int threads, int smem_bytes, void** args,
+                              cudaStream_t stream, std::atomic<uint64_t>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
+    if (done.load(std::memory_order_relaxed) & bit) {
+        e = cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem_bytes, stream);
+        if (e != cudaErrorInvalidValue) return e;
+        cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem_bytes, stream);
 }
 
 cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens);

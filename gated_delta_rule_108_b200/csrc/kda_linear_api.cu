@@ -128,6 +128,19 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a && b && x < y + nb && y < x + na;
 }
 
+struct Span { const void* p; size_t bytes; };
+
+// True where one of the `n_out` tensors overlaps another or one of the `n_in`.
+bool any_overlap(const Span* out, int n_out, const Span* in, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
+    }
+    return false;
+}
+
 LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, int B, int T, int H, int dk, int dv,
                     kda_dtype dtype, void* workspace, void* stream) {
     LinArgs a{};
@@ -206,13 +219,13 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
             return fail(KDA_ERR_INVALID_ARG, "q/k/v/o must be 16-byte aligned");
     }
     const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * T * H * dk * es, vbytes = (size_t)B * T * H * dv * es;
-    if (overlap(o, vbytes, q, kbytes) || overlap(o, vbytes, k, kbytes) || overlap(o, vbytes, v, vbytes))
-        return fail(KDA_ERR_INVALID_ARG, "o overlaps an input");
     if (!aligned16(initial_state)) return fail(KDA_ERR_INVALID_ARG, "initial_state misaligned");
     if (!aligned16(final_state)) return fail(KDA_ERR_INVALID_ARG, "final_state misaligned");
     const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
-    if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
-        return fail(KDA_ERR_INVALID_ARG, "initial_state and final_state overlap without being equal");
+    // a state may be updated in place, but not be moved by less than its size
+    const Span out[] = {{o, vbytes}, {final_state, state_bytes}};
+    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {initial_state != final_state ? initial_state : nullptr, state_bytes}};
+    if (any_overlap(out, 2, in, 4)) return fail(KDA_ERR_INVALID_ARG, "an output overlaps an input or the other output");
     st = check_workspace(workspace, workspace_bytes, p.total);
     if (st != KDA_OK) return st;
 
@@ -253,19 +266,13 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
             return fail(KDA_ERR_INVALID_ARG, "q/k/v/d_o/dq/dk/dv must be 16-byte aligned");
     }
     const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * T * H * dk * es, vbytes = (size_t)B * T * H * dv * es;
-    const void* in[4] = {q, k, v, d_o};
-    const size_t in_bytes[4] = {kbytes, kbytes, vbytes, vbytes};
-    for (int i = 0; i < 4; ++i)
-        if (overlap(dq, kbytes, in[i], in_bytes[i]) || overlap(dk_out, kbytes, in[i], in_bytes[i]) ||
-            overlap(dv_out, vbytes, in[i], in_bytes[i]))
-            return fail(KDA_ERR_INVALID_ARG, "a gradient overlaps an input");
     if (!aligned16(initial_state)) return fail(KDA_ERR_INVALID_ARG, "initial_state misaligned");
     if (!aligned16(d_final_state)) return fail(KDA_ERR_INVALID_ARG, "d_final_state misaligned");
     if (!aligned16(d_initial_state)) return fail(KDA_ERR_INVALID_ARG, "d_initial_state misaligned");
     const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
-    if (overlap(initial_state, state_bytes, d_initial_state, state_bytes) ||
-        overlap(d_final_state, state_bytes, d_initial_state, state_bytes))
-        return fail(KDA_ERR_INVALID_ARG, "d_initial_state overlaps an input state");
+    const Span out[] = {{dq, kbytes}, {dk_out, kbytes}, {dv_out, vbytes}, {d_initial_state, state_bytes}};
+    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {d_o, vbytes}, {initial_state, state_bytes}, {d_final_state, state_bytes}};
+    if (any_overlap(out, 4, in, 6)) return fail(KDA_ERR_INVALID_ARG, "a gradient overlaps an input or another gradient");
     st = check_workspace(workspace, workspace_bytes, p.total);
     if (st != KDA_OK) return st;
 
@@ -296,8 +303,10 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
         if (!q || !k || !v || !state_inout || !o) return fail(KDA_ERR_INVALID_ARG, "null pointer");
         if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state_inout) || !aligned16(o))
             return fail(KDA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
-        if (overlap(o, (size_t)B * H * dv * (dtype == KDA_BF16 ? 2 : 4), state_inout, (size_t)B * H * dk * dv * 4))
-            return fail(KDA_ERR_INVALID_ARG, "o aliases state_inout");
+        const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * H * dk * es, vbytes = (size_t)B * H * dv * es;
+        const Span out[] = {{o, vbytes}, {state_inout, (size_t)B * H * dk * dv * sizeof(float)}};
+        const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}};
+        if (any_overlap(out, 2, in, 3)) return fail(KDA_ERR_INVALID_ARG, "o or the state overlaps another tensor");
     }
     LinStepArgs a{};
     a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.state = state_inout; a.o = o;

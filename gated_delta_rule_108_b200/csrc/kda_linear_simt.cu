@@ -23,7 +23,7 @@ namespace {
 using namespace ptx;
 
 // ------------------------------------------------------------- segments --
-// Packed sequences: checks cu, orders the sequences longest first (up to 4096 of
+// Packed sequences: checks cu, orders the sequences longest first (up to 1024 of
 // them; more are taken as they come) and writes the segment table.  One segment
 // per sequence when the longest has at most `balance_tokens` tokens, the share of
 // one SM: then the sequences alone balance and the extra pass over b and c is
@@ -52,7 +52,7 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
     int32_t* order = tab + 2 + N;
     for (int s = tid; s < N; s += 1024) {
         int rank = s;
-        if (N <= 4096) {
+        if (N <= 1024) {
             const int len = cu[s + 1] - cu[s];
             rank = 0;
             for (int t = 0; t < N; ++t) {
@@ -384,15 +384,14 @@ template <int DK, int DV>
 cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
     auto kern = linear_simt_kernel<DK, DV>;
     const int smem = (int)std::max(sizeof(LinSimtSmem<DK>), sizeof(LinSimtSmem<DV>));
-    static std::atomic<uint64_t> done;
-    const cudaError_t e = lin_allow_smem(reinterpret_cast<const void*>(kern), smem, done);
-    if (e != cudaSuccess) return e;
     LinArgs b = a;
     b.slices = 1;
     for (int i = 0; i < a.roles; ++i) b.slices = std::max(b.slices, a.dim[a.role[i].c] / kSimtCols);
-    const size_t grid = (size_t)a.max_segments * a.H * a.roles * b.slices;
-    kern<<<(unsigned)grid, 256, smem, a.stream>>>(b, states_only ? 1 : 0);
-    return cudaGetLastError();
+    static std::atomic<uint64_t> done;
+    int only = states_only ? 1 : 0;
+    void* args[] = {&b, &only};
+    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * a.H * a.roles * b.slices, 256, smem,
+                      args, a.stream, done);
 }
 
 }  // namespace

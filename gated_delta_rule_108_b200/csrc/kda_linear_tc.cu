@@ -808,10 +808,9 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const uint32_t chunk = std::max(LinSmem<DK, DV>::END, LinSmem<DV, DK>::END);
     const int smem = (int)(states_only ? sum : chunk) + 1024;
     static std::atomic<uint64_t> done[2];
-    const cudaError_t e = lin_allow_smem(reinterpret_cast<const void*>(kern), smem, done[states_only]);
-    if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((size_t)a.max_segments * a.H * a.roles), states_only ? kLinSumThreads : kLinThreads, smem, a.stream>>>(p);
-    return cudaGetLastError();
+    void* args[] = {const_cast<LinTcParams*>(&p)};
+    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * a.H * a.roles,
+                      states_only ? kLinSumThreads : kLinThreads, smem, args, a.stream, done[states_only]);
 }
 
 }  // namespace

@@ -341,19 +341,22 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
  *  log_decay   [H]             fp32, <= 0; -inf forgets everything at each token;
  *              NULL: no decay (lambda = 1)
  *  initial_state, cu_seqlens, final_state, o, sizes: as kda_chunk_fwd (sequences
- *              may be empty: their final state is their initial state); o must
- *              not overlap an input
+ *              may be empty: their final state is their initial state); the
+ *              outputs must not overlap each other or an input, but final_state
+ *              may be initial_state
  *  workspace   at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
  *              aligned; its contents on entry do not matter.  Where the size is 256,
- *              the status alone, NULL is allowed: then the call has no status.  Calls that share
- *              one workspace must be ordered on one stream.
+ *              the status alone, NULL is allowed: then the call has no status.
+ *              Calls that share one workspace must be ordered on one stream.
  *              kda_workspace_status reads its status (KDA_ERR_BAD_SEQLENS,
  *              KDA_ERR_TIMEOUT).
  *
  * A sequence that is long for the number of heads and sequences is cut into
  * segments that run at the same time: one pass over k and v sums what each
- * segment adds to the state, a scan joins the sums, and the chunk kernel runs on
- * all segments with their entering states.  B*T < 2^30.
+ * segment adds to the state, the sums are joined, and the chunk kernel runs on
+ * all segments with their entering states.  Where the sequences and heads fill the
+ * GPU but do not divide evenly among its SMs, the segments of a sequence run one
+ * after another instead and nothing is summed twice.  B*T < 2^30.
  *
  * Numerics: bf16 inputs use the tensor cores with bf16 operands and fp32
  * accumulation; o differs from the exact result by about 1.4 times its own
@@ -380,7 +383,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v,
  *
  * (G_T also holds d_final_state).  Arguments as kda_linear_chunk_fwd and
  * kda_chunk_bwd; d_final_state NULL: zeros; d_initial_state NULL: not computed.
- * Outputs must not overlap inputs.
+ * Outputs must not overlap inputs or each other.
  */
 size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv,
                                            int num_seqs, int varlen, kda_dtype dtype);
@@ -395,7 +398,8 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v,
 /*
  * One token of the same recurrence for B sequences, the state updated in place.
  *  q, k [B, H, dk], v [B, H, dv] dtype; log_decay [H] fp32 or NULL;
- *  state_inout [B, H, dk, dv] fp32; o [B, H, dv] dtype (must not alias the state)
+ *  state_inout [B, H, dk, dv] fp32; o [B, H, dv] dtype; neither o nor the state
+ *  may overlap another of the tensors
  */
 kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v,
                                      const float* log_decay, float* state_inout, int B, int H,

@@ -279,9 +279,10 @@ def test_prompt_then_steps(cuda_device, dtype):
     P.assert_close(S, Sf, Sm, dtype, "state", 140, state=True)
 
 
-@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
-def test_side_stream_and_graph(cuda_device, dtype):
-    x, back = case(1, 2100, 2, 128, 128, dtype, seed=16)
+@pytest.mark.parametrize("B,T,H,dtype", [(1, 2100, 2, torch.bfloat16), (1, 2100, 2, torch.float32), (1, 2300, 50, torch.bfloat16),
+                                         (1, 100, 2, torch.bfloat16)], ids=str)
+def test_side_stream_and_graph(cuda_device, B, T, H, dtype):
+    x, back = case(B, T, H, 128, 128, dtype, seed=16)
     x, back = dev(x), dev(back)
     o, S = kda.linear_chunk_fwd(**x)
     g = kda.linear_chunk_bwd(**x, **back)
@@ -307,6 +308,49 @@ def test_side_stream_and_graph(cuda_device, dtype):
         te = kda.linear_recurrent_step(*(static[n][:, 0].contiguous() for n in "qkv"), static["log_decay"], Se)
         assert torch.equal(og, oe) and torch.equal(Sg, Se) and torch.equal(step, te)
         assert all(torch.equal(gg[n], ge[n]) for n in gg)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_two_streams_at_once(cuda_device, dtype):
+    """Calls that overlap, each with its own workspace."""
+    cases = [case(2, 900 + 100 * i, 3, 128, 128, dtype, seed=30 + i) for i in range(2)]
+    ins = [(dev(x), dev(back)) for x, back in cases]
+    ref = [(kda.linear_chunk_fwd(**x), kda.linear_chunk_bwd(**x, **b)) for x, b in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = []
+    for _ in range(5):
+        for s, (x, b) in zip(streams, ins):
+            got.append((kda.linear_chunk_fwd(**x, stream=s), kda.linear_chunk_bwd(**x, **b, stream=s)))
+    torch.cuda.synchronize()
+    for i, ((o, S), g) in enumerate(got):
+        (ro, rS), rg = ref[i % 2]
+        assert torch.equal(o, ro) and torch.equal(S, rS) and all(torch.equal(g[n], rg[n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_nan_decay_stays_with_its_head(cuda_device, dtype):
+    """Nothing waits or skips on it: the call ends, and the other heads are as they were."""
+    x, back = case(1, 3000, 3, 64, 64, dtype, seed=21)
+    x, back = dev(x), dev(back)
+    o, S = kda.linear_chunk_fwd(**x, check=True)
+    g = kda.linear_chunk_bwd(**x, **back, check=True)
+    x["log_decay"][1] = float("nan")
+    o2, S2 = kda.linear_chunk_fwd(**x, check=True)
+    g2 = kda.linear_chunk_bwd(**x, **back, check=True)
+    keep = [0, 2]
+    assert torch.equal(o[:, :, keep], o2[:, :, keep]) and torch.equal(S[:, keep], S2[:, keep])
+    assert all(torch.equal(g[n][:, :, keep], g2[n][:, :, keep]) for n in ("dq", "dk", "dv"))
+
+
+def test_many_short_sequences(cuda_device):
+    """1500 packed sequences of 0 to 5 tokens."""
+    lens = [int(n) for n in torch.randint(0, 6, (1500,), generator=torch.Generator().manual_seed(3))]
+    for dtype in DTYPES:
+        x, back = case(1, sum(lens), 1, 64, 64, dtype, lens=lens, seed=22)
+        o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+        check_fwd(x, o, S)
+        check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
 
 
 def test_training_shape_sampled(cuda_device):

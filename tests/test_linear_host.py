@@ -110,7 +110,8 @@ BAD = [(dict(dk=96), 2), (dict(dv=32), 2), (dict(dtype=7), 1), (dict(q=None), 1)
 
 @pytest.mark.parametrize("over,status", BAD + [
     (dict(o=None), 1), (dict(o=OK_PTR), 1),                            # o over q
-    (dict(s0=OK_PTR, sf=OK_PTR + 64), 1), (dict(s0=OK_PTR + 4), 1)], ids=str)
+    (dict(s0=OK_PTR, sf=OK_PTR + 64), 1), (dict(s0=OK_PTR + 4), 1),
+    (dict(o=4 * OK_PTR, s0=4 * OK_PTR + 64), 1), (dict(sf=4 * OK_PTR + 16), 1), (dict(sf=2 * OK_PTR), 1)], ids=str)
 def test_forward_refuses(lib, over, status):
     assert fwd(lib, **over) == status
     assert lib.kda_last_error()
@@ -118,7 +119,8 @@ def test_forward_refuses(lib, over, status):
 
 @pytest.mark.parametrize("over,status", BAD + [
     (dict(dq=None), 1), (dict(dq=3 * OK_PTR), 1), (dict(dvo=OK_PTR + 8), 1), (dict(s0=OK_PTR, ds0=OK_PTR), 1),
-    (dict(dsf=OK_PTR, ds0=OK_PTR + 1024), 1)], ids=str)
+    (dict(dsf=OK_PTR, ds0=OK_PTR + 1024), 1), (dict(dq=6 * OK_PTR + 64), 1), (dict(ds0=7 * OK_PTR), 1), (dict(ds0=OK_PTR), 1),
+    (dict(s0=5 * OK_PTR), 1)], ids=str)
 def test_backward_refuses(lib, over, status):
     a = dict(q=OK_PTR, k=2 * OK_PTR, v=3 * OK_PTR, ld=None, s0=None, cu=None, do=4 * OK_PTR, dsf=None, B=1, T=64, H=1, dk=64, dv=64,
              N=1, dtype=0, dq=5 * OK_PTR, dko=6 * OK_PTR, dvo=7 * OK_PTR, ds0=None, ws=OK_PTR, wsb=1 << 30)
@@ -130,7 +132,8 @@ def test_backward_refuses(lib, over, status):
 
 
 @pytest.mark.parametrize("over,status", [(dict(dk=96), 2), (dict(dtype=3), 1), (dict(S=None), 1), (dict(v=OK_PTR + 2), 1),
-                                         (dict(B=-1), 1), (dict(o=5 * OK_PTR + 16), 1), (dict(B=1 << 28), 2)], ids=str)
+                                         (dict(B=-1), 1), (dict(o=5 * OK_PTR + 16), 1), (dict(B=1 << 28), 2),
+                                         (dict(o=OK_PTR), 1), (dict(o=3 * OK_PTR + 16), 1), (dict(S=2 * OK_PTR), 1)], ids=str)
 def test_step_refuses(lib, over, status):
     a = dict(q=OK_PTR, k=2 * OK_PTR, v=3 * OK_PTR, ld=None, S=5 * OK_PTR, B=1, H=1, dk=64, dv=64, dtype=0, o=7 * OK_PTR)
     a.update(over)
