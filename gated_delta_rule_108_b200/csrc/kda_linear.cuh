@@ -35,7 +35,8 @@ struct LinRole {
     void* y;                // output [tokens, H, D2], input dtype
     const float* s_in;      // state before the first processed token, nullable (zeros)
     float* s_out;           // state after the last one, nullable
-    float* seg;             // [segments][H][D1 * D2]: each segment's own sum; after the scan its entering state
+    float* seg;             // [segments][H][D1 * D2]: each segment's own sum; after the scan its entering state;
+                            // rows of Z with fp32 inputs, columns ([D2][D1]) with bf16
     bool transposed;        // Z is the transpose of the user's [dk, dv] states
     bool reverse;           // from the last token to the first
     float c_inter, c_intra; // y_t = c_inter lambda^.. Z_0^T a_t + c_intra sum_i lambda^.. <a_t, b_i> c_i

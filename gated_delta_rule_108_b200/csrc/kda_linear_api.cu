@@ -91,7 +91,7 @@ bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, k
     const int64_t most = varlen ? (int64_t)p.N + T / p.seg_tok : (int64_t)p.N * p.num_seg;
     if (most * H * per_head >= (int64_t)1 << 31) return false;
     p.max_segments = (int)most;
-    p.balance_tokens = (int)std::min<int64_t>((int64_t)1 << 30, (int64_t)(1.6 * (double)T * H * per_head / kSms));
+    p.balance_tokens = (int)std::min<int64_t>((int64_t)1 << 30, (int64_t)(1.75 * (double)T * H * per_head / kSms));
     if (!p.split) p.balance_tokens = 1 << 30;
     p.tab_off = kHeaderBytes;
     p.flag_bytes = p.chained ? sizeof(int) * (size_t)p.max_segments * H * roles : 0;

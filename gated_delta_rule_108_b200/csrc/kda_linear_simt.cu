@@ -23,19 +23,46 @@ namespace {
 using namespace ptx;
 
 // ------------------------------------------------------------- segments --
-// Packed sequences: checks cu, orders the sequences longest first (up to 1024 of
-// them; more are taken as they come) and writes the segment table.  One segment
-// per sequence when the longest has at most `balance_tokens` tokens, the share of
-// one SM: then the sequences alone balance and the extra pass over b and c is
-// saved.
+// Exclusive sum over the block's 1024 threads.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    __syncthreads();                               // the sums of the scan before have been read
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int w = warp_sums[lane];
+        int wi = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, wi, off);
+            if (lane >= off) wi += y;
+        }
+        warp_sums[lane] = wi - w;
+    }
+    __syncthreads();
+    return warp_sums[warp] + incl - v;
+}
+
+// Packed sequences: checks cu, orders the sequences longest first, by 1024 classes of
+// length (within a class as the threads come: the order says when a segment is worked
+// on, not what it gives), and writes the segment table.  One segment per sequence when
+// the longest has at most `balance_tokens` tokens, the share of one SM: then the
+// sequences alone balance and the extra pass over b and c is saved.
 __global__ void __launch_bounds__(1024)
 linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, int N, int T, int seg_tok,
                    int balance_tokens)
 {
-    __shared__ int warp_sums[32];
-    __shared__ int s_carry, s_bad, s_max;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) { s_carry = 0; s_max = 0; s_bad = (cu[0] != 0 || cu[N] != T) ? 1 : 0; }
+    __shared__ int warp_sums[32], place[1024];
+    __shared__ int s_bad, s_max;
+    const int tid = threadIdx.x;
+    if (tid == 0) { s_max = 0; s_bad = (cu[0] != 0 || cu[N] != T) ? 1 : 0; }
+    place[tid] = 0;
     __syncthreads();
     for (int s = tid; s < N; s += 1024) {
         const int lo = cu[s], hi = cu[s + 1];
@@ -48,21 +75,16 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
         return;
     }
     const int size = s_max <= balance_tokens ? max(s_max, 1) : seg_tok;
+    const int width = s_max / 1024 + 1;
     int32_t* first = tab + 1;
     int32_t* order = tab + 2 + N;
-    for (int s = tid; s < N; s += 1024) {
-        int rank = s;
-        if (N <= 1024) {
-            const int len = cu[s + 1] - cu[s];
-            rank = 0;
-            for (int t = 0; t < N; ++t) {
-                const int lt = cu[t + 1] - cu[t];
-                rank += (lt > len) || (lt == len && t < s);
-            }
-        }
-        order[rank] = s;
-    }
+    for (int s = tid; s < N; s += 1024) atomicAdd(&place[1023 - (cu[s + 1] - cu[s]) / width], 1);
     __syncthreads();
+    place[tid] = block_scan(place[tid], warp_sums);
+    __syncthreads();
+    for (int s = tid; s < N; s += 1024) order[atomicAdd(&place[1023 - (cu[s + 1] - cu[s]) / width], 1)] = s;
+    __syncthreads();
+    int carry = 0;                                 // the same in every thread
     for (int base = 0; base < N; base += 1024) {   // exclusive scan of the segment counts
         const int r = base + tid;
         int cnt = 0;
@@ -70,33 +92,14 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
             const int s = order[r], len = cu[s + 1] - cu[s];
             cnt = len > size ? (len - 1) / size + 1 : 1;
         }
-        int incl = cnt;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        if (lane == 31) warp_sums[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            const int w = warp_sums[lane];
-            int wi = w;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, wi, off);
-                if (lane >= off) wi += y;
-            }
-            warp_sums[lane] = wi - w;
-        }
-        __syncthreads();
-        const int excl = s_carry + warp_sums[warp] + incl - cnt;
+        const int excl = carry + block_scan(cnt, warp_sums);
         if (r < N) first[r] = excl;
+        if (tid == 1023) place[0] = excl + cnt;
         __syncthreads();
-        if (tid == 1023) s_carry = excl + cnt;
-        __syncthreads();
+        carry = place[0];
     }
     if (tid == 0) {
-        first[N] = s_carry;
+        first[N] = carry;
         tab[0] = size;
         hdr->status = kStatusOk;
         hdr->runtime_err = 0;
@@ -121,9 +124,9 @@ linear_scan_kernel(const __grid_constant__ LinArgs a)
     float4 E = make_float4(0.f, 0.f, 0.f, 0.f);
     if (role.s_in) {
         const float* src = role.s_in + ((size_t)seq * a.H + h) * size;
-        if (!role.transposed) {
+        if (role.transposed == a.bf16) {        // the sums lie as the user's state does
             E = *reinterpret_cast<const float4*>(src + e);
-        } else {                                // Z is [dv, dk]: element (j, i) is the user's (i, j)
+        } else {                                // as [dv, dk]: element (j, i) is the user's (i, j)
             const int j = e / a.dk, i = e - j * a.dk;
             E = make_float4(src[(size_t)i * a.dv + j], src[(size_t)(i + 1) * a.dv + j],
                             src[(size_t)(i + 2) * a.dv + j], src[(size_t)(i + 3) * a.dv + j]);

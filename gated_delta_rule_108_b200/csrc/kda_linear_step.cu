@@ -94,7 +94,7 @@ cudaError_t launch_step_t(const LinStepArgs& a) {
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)(a.B * a.H);
     const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
-    if ((int)pairs < 2 * sms)
+    if ((int)pairs < 4 * sms)
         linear_step_kernel<T, DK, DV, 32><<<pairs * (DV / 32), 256, 0, a.stream>>>(
             q, k, v, a.log_decay, a.state, static_cast<T*>(a.o), a.scale, a.H);
     else

@@ -149,33 +149,62 @@ __device__ __forceinline__ void issue_update(uint32_t acc, uint64_t bd, uint64_t
     else issue_update_parts<D2, ROWS, 2>(acc, bd, cd, i0, first);
 }
 
-// A thread's row of Z between global memory (the user's layout or its transpose)
-// and 32 registers.
-template <int D1, int D2>
-__device__ __forceinline__ void read_state(const float* s, bool transposed, int i, int j0, float (&v)[32]) {
-    if (!s) {
+// 32 columns from j0 on of a thread's row of Z, from and to a state [D2][D1]: the lanes
+// of a warp hold rows that follow one another, so each column is one line of 128 bytes.
+// Past L1: another block of this launch may have written it.
+template <int D1>
+__device__ __forceinline__ void read_columns(const float* s, int row, int j0, float (&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-    } else if (transposed) {
+    for (int j = 0; j < 32; ++j) v[j] = __ldcg(s + (size_t)(j0 + j) * D1 + row);
+}
+template <int D1>
+__device__ __forceinline__ void write_columns(float* s, int row, int j0, const float (&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = s[(size_t)(j0 + j) * D1 + i];
-    } else {            // past L1: another block of this launch may have written it
+    for (int j = 0; j < 32; ++j) s[(size_t)(j0 + j) * D1 + row] = v[j];
+}
+
+// The same for a state [D1][D2], whose rows lie apart: four lanes take 64 bytes of a row
+// and hand them over through 2 KB of shared memory of the warp's own, 16 columns at a
+// time.  (Each lane reading its own row touches 32 lines an instruction: 8,000 cycles
+// for a state of 64 KB.)
+constexpr int kStateStage = 32 * 64;
+__device__ __forceinline__ uint32_t stage_at(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+template <int D2>
+__device__ __forceinline__ void read_rows(const float* s, unsigned char* stage, int row0, int j0, int lane, float (&v)[32]) {
+    float4 x[8];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(s + (size_t)i * D2 + j0 + j));
-            v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
+    for (int i = 0; i < 8; ++i)
+        x[i] = *reinterpret_cast<const float4*>(s + (size_t)(row0 + 8 * (i & 3) + (lane >> 2)) * D2 + j0 + 16 * (i >> 2) + 4 * (lane & 3));
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(stage + stage_at(8 * i + (lane >> 2), lane & 3)) = x[4 * half + i];
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 y = *reinterpret_cast<const float4*>(stage + stage_at(lane, c));
+            const int j = 16 * half + 4 * c;
+            v[j] = y.x; v[j + 1] = y.y; v[j + 2] = y.z; v[j + 3] = y.w;
         }
     }
 }
-template <int D1, int D2>
-__device__ __forceinline__ void write_state(float* s, bool transposed, int i, int j0, const float (&v)[32]) {
-    if (transposed) {
+template <int D2>
+__device__ __forceinline__ void write_rows(float* s, unsigned char* stage, int row0, int j0, int lane, const float (&v)[32]) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[(size_t)(j0 + j) * D1 + i] = v[j];
-    } else {
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(s + (size_t)i * D2 + j0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        for (int c = 0; c < 4; ++c) {
+            const int j = 16 * half + 4 * c;
+            *reinterpret_cast<float4*>(stage + stage_at(lane, c)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(s + (size_t)(row0 + 8 * i + (lane >> 2)) * D2 + j0 + 16 * half + 4 * (lane & 3)) =
+                *reinterpret_cast<const float4*>(stage + stage_at(8 * i + (lane >> 2), lane & 3));
     }
 }
 
@@ -222,6 +251,7 @@ struct LinSmem {
     static constexpr uint32_t CW = Z + ZB;
     static constexpr uint32_t END = CW + CWB;
     static_assert(END + 1024 + 1200 <= 232448, "shared memory");
+    static_assert(ZB >= D1 / 16 * 2048, "a state's way through Z's place");
 };
 
 constexpr int kLinThreads = 19 * 32;
@@ -278,6 +308,11 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
+    if (tid == 17 * 32) {
+        tma_prefetch_desc(&prm.map[role.b]);
+        tma_prefetch_desc(&prm.map[role.c]);
+        tma_prefetch_desc(&prm.map[role.a]);
+    }
     if (warp == 0) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
@@ -306,6 +341,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
 
     if (warp == 17) {                                   // ---- TMA loads
         if (lane == 0) {
+            tma_prefetch_desc(&prm.ymap[ri]);
             int nb = 0, nc = 0, na = 0;
             for (int n = 0; n < nch; ++n) {             // in the order in which the buffers become free
                 const int tok = g.begin + chunk_of(n) * C, i = n & 1;
@@ -501,27 +537,38 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         const int t = tid - 256;
         bool ok = true;
         const bool mine = D1 == 128 || quad < 2;        // warps with rows of Z
+        unsigned char* const stage = sm + Sm::Z + kStateStage * (D1 == 128 ? warp - 8 : 2 * sub + (quad & 1));
         if (mine) {
             const bool scanned = args.scanned && g.count > 1;
             const int before = sidx + (rev ? 1 : -1);           // the segment processed before this one
             const bool chained = args.chained && g.index != (rev ? g.count - 1 : 0);
             if (chained) ok = wait_flag(args.flags + ((size_t)before * H + h) * args.roles + ri, D1 / 16, &s_wait);
-            const float* from = chained ? role.seg + ((size_t)before * H + h) * zsize : scanned ? role.seg + ((size_t)sidx * H + h) * zsize : (role.s_in ? role.s_in + user : nullptr);
+            const float* own = chained ? role.seg + ((size_t)before * H + h) * zsize
+                             : scanned ? role.seg + ((size_t)sidx * H + h) * zsize : nullptr;
+            const float* given = role.s_in ? role.s_in + user : nullptr;
             const double l = lin_log_decay(args.log_decay, h);
 #pragma unroll 1
             for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
-                read_state<D1, D2>(from, !scanned && !chained && role.transposed, row, j0, v);
+                if (own || (given && role.transposed)) {
+                    read_columns<D1>(own ? own : given, row, j0, v);
+                } else if (given) {
+                    read_rows<D2>(given, stage, 32 * quad, j0, lane, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                }
                 if (!scanned && !args.chained)
                     lin_enter(g, sidx, rev, l, [&](int slot, float w) {
                         float u[32];
-                        read_state<D1, D2>(role.seg + ((size_t)slot * H + h) * zsize, false, row, j0, u);
+                        read_columns<D1>(role.seg + ((size_t)slot * H + h) * zsize, row, j0, u);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = fmaf(w, v[j], u[j]);
                     });
                 tmem_st32_sync(ZREG + lane_base + j0, v);
             }
         }
+        named_bar_sync(1, 256);     // Z's operand goes where the states went through (all these warps come here)
         for (int n = 0; ok && n < nch; ++n) {
             const int L = min(C, g.len - chunk_of(n) * C), len_before = n > 0 ? min(C, g.len - chunk_of(n - 1) * C) : 0;
             ok = lin_wait_warp(&full_b[n & 1], (n >> 1) & 1, &s_wait) && lin_wait_warp(&full_c[n & 1], (n >> 1) & 1, &s_wait);
@@ -591,7 +638,8 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = fmaf(gam, v[j], u[j]);
                 }
-                write_state<D1, D2>(to, !hand && role.transposed, row, j0, v);
+                if (hand || role.transposed) write_columns<D1>(to, row, j0, v);
+                else write_rows<D2>(to, stage, 32 * quad, j0, lane, v);
             }
             if (hand) raise_flag(args.flags + ((size_t)sidx * H + h) * args.roles + ri);
         }
@@ -778,10 +826,9 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
         }
         if (ok) ok = add(nch - 1);
         if (ok && (D1 == 128 || quad < 2)) {
-            float* to = role.seg + ((size_t)sidx * H + h) * D1 * D2 + (size_t)row * D2 + COLS * sub;
+            float* to = role.seg + ((size_t)sidx * H + h) * D1 * D2 + (size_t)COLS * sub * D1 + row;
 #pragma unroll
-            for (int j = 0; j < COLS; j += 4)
-                *reinterpret_cast<float4*>(to + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+            for (int j = 0; j < COLS; ++j) to[(size_t)j * D1] = z[j];
         }
     }
     tc_fence_before();
