@@ -149,6 +149,7 @@ __device__ __forceinline__ float lin_pow(double l, int n) { return (float)exp(l 
 template <class Fold>
 __device__ __forceinline__ void lin_enter(const LinMap::Seg& g, int sidx, bool rev, double l, Fold fold) {
     const int first = sidx - g.index, n = rev ? g.count - 1 - g.index : g.index;
+    if (n == 0) return;
     const float w_full = lin_pow(l, g.size), w_tail = lin_pow(l, g.tail);
     for (int i = 0; i < n; ++i) {
         const int at = rev ? g.count - 1 - i : i;
