@@ -4,13 +4,16 @@
 //   S <- lambda S + k v^T,   o = dk^{-1/2} S^T q
 //
 // The state is read once and written once, 4 dk dv bytes each way per head, and
-// that traffic bounds the step.  Each thread holds four value columns of ROWS
-// rows, so the update and the read need no exchange; the column sums are joined
-// across the lanes of a warp that share columns, then across warps.
+// that traffic bounds the step: B=256, H=32 takes 159 us, 6.8 TB/s, 3 % above a plain
+// copy's rate.  Each thread holds four value columns of ROWS rows, all loaded before
+// the first is used, so the update and the read need no exchange; the column sums are
+// joined across the lanes of a warp that share columns, then across warps.
 //
-// One CTA per (sequence, head, NS value columns).  NS = dv reads whole rows; when
-// those CTAs would leave SMs idle the columns are cut into slices of 32, which
-// puts 2 or 4 times as many SMs on the same state.
+// One CTA per (sequence, head, NS value columns).  NS = dv reads whole rows; with fewer
+// than four pairs per SM the columns are cut into slices of 32, which spreads a state
+// over 2 or 4 SMs and evens out the last wave.  Whole rows and slices, dk = dv = 128:
+// 16 pairs 2.5 and 1.7 us, 64 2.6 and 2.1, 256 4.7 and 4.7, 288 4.8 and 5.1, 320 6.3 and
+// 5.5, 512 7.8 and 7.7, 1024 13.7 and 13.8.
 #include "kda_common.cuh"
 #include "kda_linear.cuh"
 

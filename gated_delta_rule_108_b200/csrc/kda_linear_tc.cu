@@ -13,20 +13,33 @@
 // first.  Four products of 128-row tiles, all kind::f16 with bf16 operands and fp32
 // accumulators in TMEM; a, b and c are exact in bf16, so only P, Z and the
 // weighted c are rounded:
-//  - P in two bf16 parts (2^-17), the A operand in TMEM, in place of its fp32 values;
+//  - P in two bf16 parts (2^-17), the A operand in TMEM, in place of its fp32 values
+//    (one part would save 0.2 us of 4.5 us a chunk and bring o's error from 1.2 to 1.4
+//    times its own rounding);
 //  - Z in one part as operand: it only reaches y, itself bf16, and adds at most its
 //    own rounding to y's; the state itself stays fp32 in TMEM;
 //  - the weighted c in three parts (2^-25) where the state is a result, in two where
 //    it only reaches y: a state is a sum over the whole sequence, and fp32 is what
-//    it is returned in.
+//    it is returned in (two parts everywhere would save 0.4 us of 4.5 us a chunk).
+// The tensor core cuts its sums off instead of rounding them, always towards zero.
+// So each chunk's sum U starts from zero and is added to Z in registers, rounded:
+// after 16,384 tokens without decay the state is off by 1.8e-7 of its size, 5.7e-6
+// where the MMAs add to Z itself.
 //
-// One CTA per (segment, head, role), one per SM (TMEM: Z, P and two accumulators of
-// y, 512 columns).  Warp 17 loads tiles by TMA, warp 16 issues the MMAs, warps 0-7
-// weight P and write y, warps 8-15 convert and decay Z and weight c.  The chain from
-// chunk to chunk (Z -> operand -> Z^T a, update) and the rest overlap: b and c have
-// two buffers each, so the next chunk's tiles are in flight while this one is worked
-// on; a's buffer frees as soon as P and Z^T a are done; y leaves through the buffer
-// of its own chunk's c (warp 18 sends it out by TMA).
+// One CTA per (segment, head, role), one per SM: 512 columns of TMEM hold Z, U, P and
+// y.  Warp 17 loads tiles by TMA, warp 16 issues the MMAs, warps 0-7 weight P and y's
+// rows of Z^T a, weight the last quarter of c and take y out, warps 8-15 keep Z, write
+// its operand and weight the other quarters.  The chain from chunk to chunk (Z ->
+// operand -> Z^T a, U) and the rest overlap: b and c have two buffers each, so the next
+// chunk's tiles are in flight while this one is worked on; a's buffer frees as soon as
+// P and Z^T a are done; y leaves through the buffer of its own chunk's c (warp 18 sends
+// it out by TMA; stored straight from registers a chunk takes 5.2 us instead of 4.6).
+//
+// What bounds it is shared memory: a chunk's MMAs read 384 KB of operands (3,072
+// cycles), TMA moves 128 KB (1,024) and the warps 2,900 wavefronts, 7,000 cycles
+// together, and a chunk takes 6,900.  B=9, T=4096, H=16 (144 CTAs of 32 chunks): 145 us,
+// tensor pipe 52 %, issue 46 %, DRAM 4.1 TB/s; 3.8 us a chunk at the full clock, 4.5 at
+// the clock that the power limit leaves in long runs.
 //
 // Every wait is bounded; one that gives up sets a flag that ends the CTA's other
 // waits, records KDA_ERR_TIMEOUT, and the CTA waits for its own copies and MMAs,
@@ -680,7 +693,8 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 // chunk's sum is formed in TMEM (two of them, in turn) and added in registers, 32
 // elements a thread: the tensor core's cut-off sums would pile up over a long
 // segment.  Half a chunk of c is weighted, by sixteen warps, while the other half is
-// multiplied.
+// multiplied.  2.0 us a chunk, half of the chunk kernel's: the weights (three parts of
+// 128 x D2) are what it waits for.
 constexpr int kLinSumThreads = 18 * 32;
 
 template <int D1, int D2>

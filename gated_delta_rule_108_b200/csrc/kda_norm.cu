@@ -11,8 +11,11 @@
 //
 //   dx = r h - m r^3 <h, x> x,   dw = sum over tokens and heads of g r x
 //
-// Both read each row once and write it once: HBM bandwidth bounds them at size,
-// launch latency for a handful of tokens.  A lane holds eight channels of a row, in
+// Both read each row once and write it once: HBM bandwidth bounds them at size (65,536
+// tokens of 32 + 8 heads, d = 128: 227 us, 5.9 TB/s, 90 % of a plain copy's rate, issue
+// 54 %; the gradients of 4 x 4096 tokens of 16 + 16 heads 80 us, 77 %, where the weights'
+// sums hold 128 registers and leave two CTAs an SM), launch latency for a handful of
+// tokens.  A lane holds eight channels of a row, in
 // two groups of four chosen so that the two channels of a pair lie in one lane
 // (4 l.. and 4 l + rotary_dim / 2.. where halves are paired), so LPR = d / 8 lanes
 // (rounded up to 8, 16 or 32) share a row, a warp takes 32 / LPR rows at a time and
@@ -383,7 +386,8 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     a.eps = eps;
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
     // all heads of a token by one warp; fewer when the tokens alone would not give
-    // every SM sixteen warps
+    // every SM sixteen warps (40 heads, not cut / cut: 1 token 6.3 / 2.7 us, 64 7.2 / 3.0,
+    // 256 7.3 / 3.6, 1024 7.6 / 7.1; with a bound of 8 warps 256 take 3.9, of 32 4.7 us)
     const int heads = Hq + Hk, rpw = d <= 64 ? 4 : d <= 128 ? 2 : 1;
     a.slab = heads;
     while (a.slab > rpw && tokens * ((heads + a.slab - 1) / a.slab) < (int64_t)sms * 16) a.slab = (a.slab + 1) / 2;
@@ -429,7 +433,7 @@ kda_status kda_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_ou
                                 const float* q_weight, const float* k_weight, const float* inv_freq,
                                 const int32_t* positions, int B, int T, int Hq, int Hk, int d, int rotary_dim,
                                 int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_b,
-                            int64_t k_stride_t, int64_t k_stride_h, kda_dtype dtype, kda_norm norm,
+                                int64_t k_stride_t, int64_t k_stride_h, kda_dtype dtype, kda_norm norm,
                                 float eps, int interleaved, void* dq, void* dk, float* dq_weight, float* dk_weight,
                                 void* workspace, size_t workspace_bytes, void* stream) {
     const int64_t q_strides[3] = {q_stride_b, q_stride_t, q_stride_h}, k_strides[3] = {k_stride_b, k_stride_t, k_stride_h};
