@@ -162,33 +162,83 @@ linear_scan_kernel(const __grid_constant__ LinArgs a)
 // ------------------------------------------------------------ CUDA cores --
 constexpr int kSimtChunk = 64, kSimtCols = 64;   // tokens per chunk, value columns per CTA
 
+// Rows of 16-byte groups whose place within a row depends on the row, so that the eight
+// lanes of a 16-byte access fall on different banks: in a and b two rows eight apart with
+// four groups each, or four rows four apart; in c and Z four rows four apart with two
+// groups each.
 template <int D1>
 struct LinSimtSmem {
-    static constexpr int LDA = D1 + 4;           // rows 16 bytes apart in the banks: float4 reads of 8 rows do not clash
-    static constexpr int LDC = kSimtCols, LDP = kSimtChunk + 4;
-    struct Tile { float a[kSimtChunk][LDA], b[kSimtChunk][LDA], c[kSimtChunk][LDC]; } tile[2];
-    float p[kSimtChunk][LDP], z[D1][LDC];
+    struct Tile { float a[kSimtChunk * D1], b[kSimtChunk * D1], c[kSimtChunk * kSimtCols]; } tile[2];
+    float p[kSimtChunk * kSimtChunk], z[D1 * kSimtCols];
     float pw[kSimtChunk + 1];
+
+    static __device__ __forceinline__ int at(int r, int group) {          // a, b
+        return r * D1 + 4 * (group ^ (((r >> 2) & 3) | ((r >> 1) & 4)));
+    }
+    static __device__ __forceinline__ int at_c(int r, int group) {        // c, Z
+        return r * kSimtCols + 4 * (group ^ (((r >> 2) & 3) << 1));
+    }
 };
 
-// y += p c, a row's four columns.
-__device__ __forceinline__ void axpy(float2 (&y)[2], float p, const float4& c) {
-    y[0] = fma2(make_float2(p, p), make_float2(c.x, c.y), y[0]);
-    y[1] = fma2(make_float2(p, p), make_float2(c.z, c.w), y[1]);
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// Sums of the four lanes 4 n .. 4 n + 3 over eight rows of eight values, two rows left to
+// each: rows 4 bit0 + 2 bit1 + {0, 1} of the lane's number.
+__device__ __forceinline__ void sum_of_four(const float2 (&x)[8][4], int lane, float2 (&y)[2][4]) {
+    float2 h[4][4];
+    const bool hi = lane & 1, up = lane & 2;
+    auto swap = [](float2 keep, float2 send, int mask) {
+        return make_float2(keep.x + __shfl_xor_sync(0xffffffffu, send.x, mask), keep.y + __shfl_xor_sync(0xffffffffu, send.y, mask));
+    };
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[m][k] = swap(hi ? x[m + 4][k] : x[m][k], hi ? x[m][k] : x[m + 4][k], 1);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[m][k] = swap(up ? h[m + 2][k] : h[m][k], up ? h[m][k] : h[m + 2][k], 2);
 }
 
-// One CTA per (segment, head, 64 columns of D2); 256 threads.  A thread owns 4 x 4
-// of P and of y (rows ty + 16 n) and D1 / 16 x 4 of Z, which stays in registers
-// with a copy in shared memory for the read.  Bound by FMA issue (two at a time,
-// 32 instructions per 8 16-byte shared-memory reads); the next chunk's tiles arrive
-// by cp.async meanwhile, rows past a segment's end as zeros.
+// y[m] += p[m] * (eight columns in c0, c1), eight rows.
+__device__ __forceinline__ void outer(float2 (&y)[8][4], const float (&p)[8], const float4& c0, const float4& c1) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const float2 q = make_float2(p[m], p[m]);
+        y[m][0] = fma2(q, make_float2(c0.x, c0.y), y[m][0]);
+        y[m][1] = fma2(q, make_float2(c0.z, c0.w), y[m][1]);
+        y[m][2] = fma2(q, make_float2(c1.x, c1.y), y[m][2]);
+        y[m][3] = fma2(q, make_float2(c1.z, c1.w), y[m][3]);
+    }
+}
+// Four steps of that, the rows' factors contiguous in memory.
+__device__ __forceinline__ void outer4(float2 (&y)[8][4], const float4 (&a)[8], const float* c, const int (&c_at)[4][2]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float p[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) p[m] = e == 0 ? a[m].x : e == 1 ? a[m].y : e == 2 ? a[m].z : a[m].w;
+        outer(y, p, lds4(c + c_at[e][0]), lds4(c + c_at[e][1]));
+    }
+}
+
+// One CTA per (segment, head, 64 columns of D2); 256 threads, a warp for every eighth
+// row.  Every product of a chunk gives tiles of 64 x 64, a thread 8 x 8 of them from a
+// quarter of the terms: the four lanes of one place share them out by groups of four and
+// join their sums by shuffles.  Two things hold it: FMA issue, and the way from shared
+// memory into registers, 128 bytes a cycle whatever the lanes share, of which 8 x 8 takes
+// 16 16-byte reads for 128 paired FMAs.  B=4, T=4096, H=16, dk = dv = 128: 968 us, FMA
+// pipes 56 %, reads 47 %, and the two warps of a scheduler do not fill the gaps; 8 x 4 by
+// 512 threads takes 1,084 us (reads 62 %), 4 x 4 without the quarters 978 (dk = dv = 64:
+// 8 x 8 574, 4 x 4 664).  The next chunk's tiles arrive by cp.async meanwhile, rows past a
+// segment's end as zeros.
 template <int D1, int D2>
 __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, int x, int states_only)
 {
     using Sm = LinSimtSmem<D1>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
-    constexpr int SL = D2 / kSimtCols, ZR = D1 / 16;
+    constexpr int SL = D2 / kSimtCols, HALVES = D1 / 64;
     const int slice = x % args.slices;
     x /= args.slices;
     if (slice >= SL) return;                     // a role with fewer columns than another
@@ -200,7 +250,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
     const bool last = g.index == (rev ? 0 : g.count - 1);        // the segment processed last
     if (states_only && last) return;
     const int j0 = slice * kSimtCols;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int tid = threadIdx.x, lane = tid & 31, ty = tid >> 5, tx = lane >> 2, part = lane & 3;
     const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
     for (int n = tid; n <= kSimtChunk; n += 256) sm.pw[n] = lin_pow(l, n);
@@ -220,44 +270,54 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
             typename Sm::Tile& t = sm.tile[n & 1];
             const int off = chunk_of(n) * kSimtChunk, L = min(kSimtChunk, g.len - off), tok0 = g.begin + off;
             for (int e = tid; e < kSimtChunk * (D1 / 4); e += 256) {
-                const int r = e / (D1 / 4), i = 4 * (e % (D1 / 4));
-                const size_t at = ((size_t)(tok0 + min(r, L - 1)) * H + h) * D1 + i;
-                cp_async16(&t.b[r][i], pb + at, r < L ? 16 : 0);
-                if (!states_only) cp_async16(&t.a[r][i], pa + at, r < L ? 16 : 0);
+                const int r = e / (D1 / 4), i = e % (D1 / 4);
+                const size_t at = ((size_t)(tok0 + min(r, L - 1)) * H + h) * D1 + 4 * i;
+                cp_async16(t.b + Sm::at(r, i), pb + at, r < L ? 16 : 0);
+                if (!states_only) cp_async16(t.a + Sm::at(r, i), pa + at, r < L ? 16 : 0);
             }
             for (int e = tid; e < kSimtChunk * (kSimtCols / 4); e += 256) {
-                const int r = e / (kSimtCols / 4), j = 4 * (e % (kSimtCols / 4));
-                cp_async16(&t.c[r][j], pc + ((size_t)(tok0 + min(r, L - 1)) * H + h) * D2 + j0 + j, r < L ? 16 : 0);
+                const int r = e / (kSimtCols / 4), j = e % (kSimtCols / 4);
+                cp_async16(t.c + Sm::at_c(r, j), pc + ((size_t)(tok0 + min(r, L - 1)) * H + h) * D2 + j0 + 4 * j, r < L ? 16 : 0);
             }
         }
         cp_async_commit();
     };
     fetch(0);
 
-    float2 z[ZR][2];
+    // this thread's part of Z: rows row_z(half, 0 and 1), columns 4 tx.. and 32 + 4 tx..
+    auto row_z = [&](int half, int m) { return 64 * half + 32 * (part & 1) + 4 * ty + (part & 2) + m; };
+    float2 z[HALVES][2][4];
     const bool scanned = args.scanned && g.count > 1;
     const float* from = states_only ? nullptr : (scanned ? seg : (role.s_in ? role.s_in + user : nullptr));
     const bool tr_in = !scanned && role.transposed;
 #pragma unroll
-    for (int n = 0; n < ZR; ++n) {
-        const int i = ty * ZR + n, j = j0 + 4 * tx;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (from)
-            v = tr_in ? make_float4(from[(size_t)j * D1 + i], from[(size_t)(j + 1) * D1 + i],
-                                    from[(size_t)(j + 2) * D1 + i], from[(size_t)(j + 3) * D1 + i])
-                      : *reinterpret_cast<const float4*>(from + (size_t)i * D2 + j);
-        z[n][0] = make_float2(v.x, v.y);
-        z[n][1] = make_float2(v.z, v.w);
-    }
+    for (int n = 0; n < HALVES; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int i = row_z(n, m), j = j0 + 32 * q + 4 * tx;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (from)
+                    v = tr_in ? make_float4(from[(size_t)j * D1 + i], from[(size_t)(j + 1) * D1 + i],
+                                            from[(size_t)(j + 2) * D1 + i], from[(size_t)(j + 3) * D1 + i])
+                              : *reinterpret_cast<const float4*>(from + (size_t)i * D2 + j);
+                z[n][m][2 * q] = make_float2(v.x, v.y);
+                z[n][m][2 * q + 1] = make_float2(v.z, v.w);
+            }
     if (!states_only && !scanned)
         lin_enter(g, sidx, rev, l, [&](int slot, float w) {
-            const float* own = role.seg + ((size_t)slot * H + h) * zsize + (size_t)ty * ZR * D2 + j0 + 4 * tx;
+            const float* own = role.seg + ((size_t)slot * H + h) * zsize;
 #pragma unroll
-            for (int n = 0; n < ZR; ++n) {
-                const float4 u = *reinterpret_cast<const float4*>(own + (size_t)n * D2);
-                z[n][0] = fma2(make_float2(w, w), z[n][0], make_float2(u.x, u.y));
-                z[n][1] = fma2(make_float2(w, w), z[n][1], make_float2(u.z, u.w));
-            }
+            for (int n = 0; n < HALVES; ++n)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float4 u = *reinterpret_cast<const float4*>(own + (size_t)row_z(n, m) * D2 + j0 + 32 * q + 4 * tx);
+                        z[n][m][2 * q] = fma2(make_float2(w, w), z[n][m][2 * q], make_float2(u.x, u.y));
+                        z[n][m][2 * q + 1] = fma2(make_float2(w, w), z[n][m][2 * q + 1], make_float2(u.z, u.w));
+                    }
         });
     for (int n = 0; n < nch; ++n) {
         const int ch = chunk_of(n);
@@ -266,119 +326,158 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
         cp_async_wait<0>();
         if (!states_only) {
 #pragma unroll
-            for (int i = 0; i < ZR; ++i)
-                *reinterpret_cast<float4*>(&sm.z[ty * ZR + i][4 * tx]) = make_float4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
+            for (int k = 0; k < HALVES; ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        *reinterpret_cast<float4*>(sm.z + Sm::at_c(row_z(k, m), 8 * q + tx)) =
+                            make_float4(z[k][m][2 * q].x, z[k][m][2 * q].y, z[k][m][2 * q + 1].x, z[k][m][2 * q + 1].y);
         }
         __syncthreads();                         // chunk n has landed; chunk n - 1 has been read by all
         fetch(n + 1);
         if (!states_only) {
-            float2 acc[4][4] = {};
-#pragma unroll 4
-            for (int i = 0; i < D1; i += 4) {
-                float4 av[4], bv[4];
+            // P: rows ty + 8 m, columns 8 tx + k, channels in groups of four, every fourth group
+            {
+                float2 acc[8][8] = {};
+#pragma unroll 1
+                for (int i = part; i < D1 / 4; i += 4) {
+                    float4 av[8];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    av[m] = *reinterpret_cast<const float4*>(&t.a[ty + 16 * m][i]);
-                    bv[m] = *reinterpret_cast<const float4*>(&t.b[tx + 16 * m][i]);
-                }
+                    for (int m = 0; m < 8; ++m) av[m] = lds4(t.a + Sm::at(ty + 8 * m, i));
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 bv = lds4(t.b + Sm::at(8 * tx + k, i));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        acc[m][k] = fma2(make_float2(av[m].x, av[m].y), make_float2(bv[k].x, bv[k].y), acc[m][k]);
-                        acc[m][k] = fma2(make_float2(av[m].z, av[m].w), make_float2(bv[k].z, bv[k].w), acc[m][k]);
+                        for (int m = 0; m < 8; ++m) {
+                            acc[m][k] = fma2(make_float2(av[m].x, av[m].y), make_float2(bv.x, bv.y), acc[m][k]);
+                            acc[m][k] = fma2(make_float2(av[m].z, av[m].w), make_float2(bv.z, bv.w), acc[m][k]);
+                        }
                     }
+                }
+                float2 sum[8][4], own[2][4];
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sum[m][k] = make_float2(acc[m][2 * k].x + acc[m][2 * k].y, acc[m][2 * k + 1].x + acc[m][2 * k + 1].y);
+                sum_of_four(sum, lane, own);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int r = ty + 8 * (4 * (part & 1) + (part & 2) + m);
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int lag = rev ? 8 * tx + k - r : r - 8 * tx - k;
+                        v[k] = lag >= 0 ? c_intra * sm.pw[lag] * (k & 1 ? own[m][k >> 1].y : own[m][k >> 1].x) : 0.f;
+                    }
+                    float* dst = sm.p + r * kSimtChunk + 8 * tx;
+                    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            __syncwarp();                        // a warp reads the rows of P that it has written
+            float2 out[8][4] = {};
+#pragma unroll 1
+            for (int i = part; i < D1 / 4; i += 4) {
+                float4 av[8];
+                int at[4][2];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) av[m] = lds4(t.a + Sm::at(ty + 8 * m, i));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    at[e][0] = Sm::at_c(4 * i + e, tx);
+                    at[e][1] = Sm::at_c(4 * i + e, 8 + tx);
+                }
+                outer4(out, av, sm.z, at);
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int lag = rev ? (tx + 16 * k) - (ty + 16 * m) : (ty + 16 * m) - (tx + 16 * k);
-                    sm.p[ty + 16 * m][tx + 16 * k] = lag >= 0 ? c_intra * sm.pw[lag] * (acc[m][k].x + acc[m][k].y) : 0.f;
-                }
-            __syncthreads();
-            float2 out[4][2] = {};
-#pragma unroll 4
-            for (int i = 0; i < D1; i += 4) {
-                const float4 c0 = *reinterpret_cast<const float4*>(&sm.z[i][4 * tx]);
-                const float4 c1 = *reinterpret_cast<const float4*>(&sm.z[i + 1][4 * tx]);
-                const float4 c2 = *reinterpret_cast<const float4*>(&sm.z[i + 2][4 * tx]);
-                const float4 c3 = *reinterpret_cast<const float4*>(&sm.z[i + 3][4 * tx]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float4 p = *reinterpret_cast<const float4*>(&t.a[ty + 16 * m][i]);
-                    axpy(out[m], p.x, c0); axpy(out[m], p.y, c1); axpy(out[m], p.z, c2); axpy(out[m], p.w, c3);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = ty + 16 * m;
+            for (int m = 0; m < 8; ++m) {
+                const int r = ty + 8 * m;
                 const float w = c_inter * sm.pw[r < L ? (rev ? L - 1 - r : r + 1) : 0];
-                out[m][0] = mul2(make_float2(w, w), out[m][0]);
-                out[m][1] = mul2(make_float2(w, w), out[m][1]);
-            }
-#pragma unroll 4
-            for (int i = 0; i < kSimtChunk; i += 4) {
-                const float4 c0 = *reinterpret_cast<const float4*>(&t.c[i][4 * tx]);
-                const float4 c1 = *reinterpret_cast<const float4*>(&t.c[i + 1][4 * tx]);
-                const float4 c2 = *reinterpret_cast<const float4*>(&t.c[i + 2][4 * tx]);
-                const float4 c3 = *reinterpret_cast<const float4*>(&t.c[i + 3][4 * tx]);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float4 p = *reinterpret_cast<const float4*>(&sm.p[ty + 16 * m][i]);
-                    axpy(out[m], p.x, c0); axpy(out[m], p.y, c1); axpy(out[m], p.z, c2); axpy(out[m], p.w, c3);
+                for (int k = 0; k < 4; ++k) out[m][k] = mul2(make_float2(w, w), out[m][k]);
+            }
+#pragma unroll 1
+            for (int i = part; i < kSimtChunk / 4; i += 4) {
+                float4 pv[8];
+                int at[4][2];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) pv[m] = lds4(sm.p + (ty + 8 * m) * kSimtChunk + 4 * i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    at[e][0] = Sm::at_c(4 * i + e, tx);
+                    at[e][1] = Sm::at_c(4 * i + e, 8 + tx);
+                }
+                outer4(out, pv, t.c, at);
+            }
+            float2 own[2][4];
+            sum_of_four(out, lane, own);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int r = ty + 8 * (4 * (part & 1) + (part & 2) + m);
+                if (r >= L) continue;
+                float* dst = py + ((size_t)(tok0 + r) * H + h) * D2 + j0 + 4 * tx;
+                *reinterpret_cast<float4*>(dst) = make_float4(own[m][0].x, own[m][0].y, own[m][1].x, own[m][1].y);
+                *reinterpret_cast<float4*>(dst + 32) = make_float4(own[m][2].x, own[m][2].y, own[m][3].x, own[m][3].y);
+            }
+            __syncthreads();                     // Z has been read by all: the next chunk's goes in its place
+        }
+        // the chunk's sum: rows 4 ty.. and 32 + 4 ty.. of each half, tokens in groups of four
+        const float2 w = make_float2(sm.pw[L], sm.pw[L]);
+#pragma unroll
+        for (int half = 0; half < HALVES; ++half) {
+            float2 u[8][4] = {}, own[2][4];
+#pragma unroll 1
+            for (int q = part; q < kSimtChunk / 4; q += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 4 * q + e;
+                    const float m = r < L ? c_upd * sm.pw[rev ? r + 1 : L - 1 - r] : 0.f;
+                    const float4 b0 = lds4(t.b + Sm::at(r, 16 * half + ty)), b1 = lds4(t.b + Sm::at(r, 16 * half + 8 + ty));
+                    const float b[8] = {m * b0.x, m * b0.y, m * b0.z, m * b0.w, m * b1.x, m * b1.y, m * b1.z, m * b1.w};
+                    outer(u, b, lds4(t.c + Sm::at_c(r, tx)), lds4(t.c + Sm::at_c(r, 8 + tx)));
                 }
             }
+            sum_of_four(u, lane, own);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = ty + 16 * m;
-                if (r < L)
-                    *reinterpret_cast<float4*>(py + ((size_t)(tok0 + r) * H + h) * D2 + j0 + 4 * tx) =
-                        make_float4(out[m][0].x, out[m][0].y, out[m][1].x, out[m][1].y);
-            }
-        }
-        const float w = sm.pw[L];
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < ZR; ++i) {
-            z[i][0] = mul2(make_float2(w, w), z[i][0]);
-            z[i][1] = mul2(make_float2(w, w), z[i][1]);
-        }
-#pragma unroll 4
-        for (int r = 0; r < kSimtChunk; ++r) {
-            const float m = r < L ? c_upd * sm.pw[rev ? r + 1 : L - 1 - r] : 0.f;
-            float4 c = *reinterpret_cast<const float4*>(&t.c[r][4 * tx]);
-            c.x *= m; c.y *= m; c.z *= m; c.w *= m;
-#pragma unroll
-            for (int i = 0; i < ZR; i += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(&t.b[r][ty * ZR + i]);
-                axpy(z[i], b.x, c); axpy(z[i + 1], b.y, c); axpy(z[i + 2], b.z, c); axpy(z[i + 3], b.w, c);
-            }
+                for (int k = 0; k < 4; ++k) z[half][m][k] = fma2(w, z[half][m][k], own[m][k]);
         }
     }
     float* to = states_only ? seg : (last && role.s_out ? role.s_out + user : nullptr);
     if (!to) return;
     const bool tr_out = !states_only && role.transposed;
 #pragma unroll
-    for (int n = 0; n < ZR; ++n) {
-        const int i = ty * ZR + n, j = j0 + 4 * tx;
-        if (tr_out) {
-            to[(size_t)j * D1 + i] = z[n][0].x;
-            to[(size_t)(j + 1) * D1 + i] = z[n][0].y;
-            to[(size_t)(j + 2) * D1 + i] = z[n][1].x;
-            to[(size_t)(j + 3) * D1 + i] = z[n][1].y;
-        } else {
-            *reinterpret_cast<float4*>(to + (size_t)i * D2 + j) = make_float4(z[n][0].x, z[n][0].y, z[n][1].x, z[n][1].y);
-        }
-    }
+    for (int n = 0; n < HALVES; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int i = row_z(n, m), j = j0 + 32 * q + 4 * tx;
+                const float2 lo = z[n][m][2 * q], hi = z[n][m][2 * q + 1];
+                if (tr_out) {
+                    to[(size_t)j * D1 + i] = lo.x;
+                    to[(size_t)(j + 1) * D1 + i] = lo.y;
+                    to[(size_t)(j + 2) * D1 + i] = hi.x;
+                    to[(size_t)(j + 3) * D1 + i] = hi.y;
+                } else {
+                    *reinterpret_cast<float4*>(to + (size_t)i * D2 + j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
 }
 
-// One launch for all roles: those over (DK, DV) and those over (DV, DK).
+// One launch for all roles: those over (DK, DV) and those over (DV, DK), one after the
+// other, those with more rows of Z and so more work a block first (gradients of B=4,
+// T=1021, H=16, dk 64, dv 128: 401 us, 509 with the roles in turn).
 template <int DK, int DV>
 __global__ void __launch_bounds__(256, 1)
 linear_simt_kernel(const __grid_constant__ LinArgs args, int states_only)
 {
     if (!lin_begin(args)) return;
-    const int ri = blockIdx.x % args.roles, x = blockIdx.x / args.roles;
+    const int blocks = gridDim.x / args.roles, nth = blockIdx.x / blocks, x = blockIdx.x % blocks;
+    const int ri = DK > DV ? args.roles - 1 - nth : nth;
     if (DK == DV || !args.role[ri].transposed) linear_simt_body<DK, DV>(args, ri, x, states_only);
     else linear_simt_body<DV, DK>(args, ri, x, states_only);
 }
