@@ -353,6 +353,48 @@ def test_many_short_sequences(cuda_device):
         check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
 
 
+def test_offsets_past_31_bits(cuda_device):
+    """q, k, v and o of more than 2^31 elements each: the short sequence behind the long one, and the norm there."""
+    lens, H, d = (524300, 200), 32, 128
+    T = sum(lens)
+    assert lens[0] * H * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q, k, v, d_o = (torch.randn(1, T, H, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    cu = torch.tensor([0, lens[0], T], dtype=torch.int32, device="cuda")
+    qn, kn = kda.qk_norm_rope(q, k, inv_freq=torch.ones(16, device="cuda"))
+    pos = torch.arange(T - 200, T, dtype=torch.int32, device="cuda")[None]
+    part = kda.qk_norm_rope(q[:, -200:], k[:, -200:], inv_freq=torch.ones(16, device="cuda"), positions=pos)
+    assert torch.equal(qn[:, -200:], part[0]) and torch.equal(kn[:, -200:], part[1])
+    del q, k, part
+    log_decay = decays("slopes", H)
+    o, S = kda.linear_chunk_fwd(qn, kn, v, log_decay.cuda(), cu_seqlens=cu, check=True)
+    r = kda.linear_chunk_bwd(qn, kn, v, log_decay.cuda(), d_o, cu_seqlens=cu, check=True)
+    for h in (0, H - 1):
+        tail = lambda t: t[:, -200:, h:h + 1].cpu()  # noqa: E731
+        x = dict(q=tail(qn), k=tail(kn), v=tail(v), log_decay=log_decay[h:h + 1], initial_state=None, cu_seqlens=None)
+        check_fwd(x, tail(o), S[1:, h:h + 1].cpu())
+        back = dict(d_o=tail(d_o), d_final_state=torch.zeros(1, 1, d, d))
+        check_bwd(x, back, {**{n: tail(r[n]) for n in ("dq", "dk", "dv")}, "dS0": r["dS0"][1:, h:h + 1].cpu()})
+
+
+@pytest.mark.parametrize("B,H", [(37, 16), (74, 8), (9, 32)])
+def test_step_slices(cuda_device, B, H):
+    """Around 592 pairs: states cut into slices of columns, and whole ones."""
+    x, _ = case(B, 1, H, 128, 128, torch.bfloat16, seed=24)
+    d = dev(x)
+    S = d["initial_state"].clone()
+    o = kda.linear_recurrent_step(*(d[n][:, 0] for n in "qkv"), d["log_decay"], S)
+    few, Sf = [], []
+    for b in range(B):      # every sequence by itself
+        s = d["initial_state"][b:b + 1].clone()
+        few.append(kda.linear_recurrent_step(*(d[n][b:b + 1, 0] for n in "qkv"), d["log_decay"], s))
+        Sf.append(s)
+    assert torch.equal(S, torch.cat(Sf))
+    # sums over the same products in another order: dk roundings of the largest partial sum
+    _, _, om, _ = plain(x)
+    assert ((o - torch.cat(few)).abs().cpu().double() <= 2.0 ** -7 * o.abs().cpu().double() + 144 * 2.0 ** -24 * om[:, 0]).all()
+
+
 def test_training_shape_sampled(cuda_device):
     """B=4, T=4096, H=16, bf16: two (sequence, head) pairs of the forward and the gradients."""
     x, back = case(4, 4096, 16, 128, 128, torch.bfloat16, seed=17)

@@ -156,6 +156,67 @@ def test_own_positions_and_no_tokens(cuda_device, dtype):
     assert not r["dq_weight"].any() and not r["dk_weight"].any()
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_shared_heads_and_positions_below_zero(cuda_device, dtype):
+    """Keys of one head, and queries of one batch row, seen by all (strides of zero)."""
+    x, dy, qkv = case(3, 17, 4, 2, 64, 32, dtype, seed=8)
+    x["positions"] = -torch.arange(3 * 17, dtype=torch.int32).view(3, 17) * 1000
+    x["k"], x["q"] = x["k"][:, :, :1].expand(3, 17, 2, 64), x["q"][:1].expand(3, 17, 4, 64)
+    d = {n: None if t is None else t.cuda() for n, t in x.items()}
+    joint = qkv.cuda()
+    d["k"], d["q"] = joint[:, :, 4:5].expand(3, 17, 2, 64), joint[:1, :, :4].expand(3, 17, 4, 64)
+    assert d["k"].stride(2) == 0 and d["q"].stride(0) == 0
+    check(x, kda.qk_norm_rope(**d), "l2", 1e-6, False)
+    flat = {**d, "q": d["q"].contiguous(), "k": d["k"].contiguous()}
+    r = kda.qk_norm_rope_bwd(**d, d_q_out=dy[0].cuda(), d_k_out=dy[1].cuda())
+    f = kda.qk_norm_rope_bwd(**flat, d_q_out=dy[0].cuda(), d_k_out=dy[1].cuda())
+    assert all(torch.equal(r[n], f[n]) for n in r)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_bad_rows_stay_their_own(cuda_device, dtype, interleaved):
+    """NaN and infinities of one head of one token reach no other row."""
+    x, dy, qkv = case(2, 40, 3, 2, 128, 64, dtype, seed=9)
+    d, dy = dev(x, qkv), [t.cuda() for t in dy]
+    kw = dict(d_q_out=dy[0], d_k_out=dy[1], interleaved=interleaved)
+    y, r = kda.qk_norm_rope(**d, interleaved=interleaved), kda.qk_norm_rope_bwd(**d, **kw)
+    bad = qkv.clone()
+    bad[1, 7, 1] = float("nan")
+    bad[0, 3, 4, 5] = float("inf")
+    b = dev(x, bad)
+    y2, r2 = kda.qk_norm_rope(**b, interleaved=interleaved), kda.qk_norm_rope_bwd(**b, **kw)
+    keep_q, keep_k = (torch.ones(2, 40, n, dtype=torch.bool, device="cuda") for n in (3, 2))
+    keep_q[1, 7, 1] = keep_k[0, 3, 1] = False
+    for a, c in ((y, y2), ((r["dq"], r["dk"]), (r2["dq"], r2["dk"]))):
+        assert torch.equal(a[0][keep_q], c[0][keep_q]) and torch.equal(a[1][keep_k], c[1][keep_k])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_two_streams_and_two_graphs(cuda_device, dtype):
+    """Calls that overlap, each with a workspace of its own, and two captured calls that share one, in turn."""
+    cases = [case(1, 500 + 100 * i, 4, 2, 128, 128, dtype, seed=10 + i) for i in range(2)]
+    ins = [({**dev(x, qkv)}, dict(d_q_out=dy[0].cuda(), d_k_out=dy[1].cuda())) for x, dy, qkv in cases]
+    ref = [kda.qk_norm_rope_bwd(**d, **g) for d, g in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [kda.qk_norm_rope_bwd(**d, **g, stream=s) for _ in range(5) for s, (d, g) in zip(streams, ins)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(r[n], ref[i % 2][n]) for n in r)
+    ws = torch.empty(kda.lib().kda_qk_norm_rope_bwd_workspace_size(128), dtype=torch.uint8, device="cuda")
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in ins], []
+    for graph, (d, g) in zip(graphs, ins):
+        with torch.cuda.graph(graph):
+            outs.append(kda.qk_norm_rope_bwd(**d, **g, workspace=ws))
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for r, e in zip(outs, ref):
+        assert all(torch.equal(r[n], e[n]) for n in r)
+
+
 def test_only_one_weight(cuda_device):
     x, dy, qkv = case(1, 50, 2, 2, 64, 0, torch.float32, seed=6)
     x["q_weight"] = None
