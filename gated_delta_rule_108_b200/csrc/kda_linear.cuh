@@ -39,7 +39,7 @@ struct LinRole {
     void* y;                // output [tokens, H, D2], input dtype
     const float* s_in;      // state before the first processed token, nullable (zeros)
     float* s_out;           // state after the last one, nullable
-    float* seg;             // [segments][H][D1 * D2]: each segment's own sum; after the scan its entering state;
+    float* seg;             // [segments][pieces][H][D1 * D2]: each segment's own sum; after the scan its entering state;
                             // rows of Z with fp32 inputs, columns ([D2][D1]) with bf16
     bool transposed;        // Z is the transpose of the user's [dk, dv] states
     bool reverse;           // from the last token to the first
@@ -54,7 +54,8 @@ struct LinRole {
 // values first sums every segment's own contribution to the state, and a scan
 // turns those into the states that enter each segment, so that all segments run
 // at the same time.  With few segments (kLinDirect) each CTA forms its entering state
-// from the sums of the segments before it, and there is no scan.
+// from the sums of the segments before it, and there is no scan; then a segment may be
+// summed in pieces, where the segments alone would leave SMs without work in that pass.
 // Or the segments of a sequence run one after another, each starting from the state
 // that the one before has left in memory (LinArgs::chained): nothing is summed twice,
 // and chains that do not divide evenly among the SMs still do.
@@ -65,12 +66,16 @@ struct LinMap {
     const int32_t* tab;
     int N, T;               // T: tokens per sequence, or in all when packed
     int seg_tok, num_seg;   // not packed: tokens per segment, segments per sequence
+    int pieces;             // sums per segment, 1 where a scan follows
 
     struct Seg {
         int seq, begin, len;      // sequence, first token in the flat token order, tokens
         int index, count;         // which segment of how many of its sequence
         int size, tail;           // tokens of each of them, and of the last one
     };
+    __device__ __forceinline__ int piece_tok(int size) const {   // tokens of a piece, whole chunks
+        return pieces == 1 ? size : ((size + kLinChunk - 1) / kLinChunk + pieces - 1) / pieces * kLinChunk;
+    }
     __device__ __forceinline__ int segments() const { return cu ? tab[1 + N] : N * num_seg; }
     __device__ __forceinline__ void range(int r, int& seq, int& first, int& count) const {   // r-th sequence's segments
         if (!cu) {
@@ -101,6 +106,14 @@ struct LinMap {
         g.len = min(size, seq_len - off);
         g.size = size;
         g.tail = seq_len - (g.count - 1) * size;
+        return g;
+    }
+    // Segment s / pieces cut down to its piece s % pieces (len <= 0: an empty one).
+    __device__ __forceinline__ Seg locate_piece(int s) const {
+        Seg g = locate(s / pieces);
+        const int tok = piece_tok(g.size), off = s % pieces * tok;
+        g.begin += off;
+        g.len = min(tok, g.len - off);
         return g;
     }
 };
@@ -151,13 +164,17 @@ __device__ __forceinline__ float lin_pow(double l, int n) { return (float)exp(l 
 // The sums before segment g of a sequence, in processing order: `fold(slot, w)` is to
 // make E = w E + (the sum in that slot), E beginning as the initial state.
 template <class Fold>
-__device__ __forceinline__ void lin_enter(const LinMap::Seg& g, int sidx, bool rev, double l, Fold fold) {
-    const int first = sidx - g.index, n = rev ? g.count - 1 - g.index : g.index;
-    if (n == 0) return;
-    const float w_full = lin_pow(l, g.size), w_tail = lin_pow(l, g.tail);
-    for (int i = 0; i < n; ++i) {
-        const int at = rev ? g.count - 1 - i : i;
-        fold(first + at, at == g.count - 1 ? w_tail : w_full);
+__device__ __forceinline__ void lin_enter(const LinMap& map, const LinMap::Seg& g, int sidx, bool rev, double l, Fold fold) {
+    const int first = sidx - g.index, n = rev ? g.count - 1 - g.index : g.index, tok = map.piece_tok(g.size);
+    int w_len = 0;
+    float w = 1.f;
+    for (int i = 0; i < n * map.pieces; ++i) {
+        const int seg = rev ? g.count - 1 - i / map.pieces : i / map.pieces;
+        const int piece = rev ? map.pieces - 1 - i % map.pieces : i % map.pieces;
+        const int len = min(tok, (seg == g.count - 1 ? g.tail : g.size) - piece * tok);
+        if (len <= 0) continue;
+        if (len != w_len) w = lin_pow(l, w_len = len);
+        fold((first + seg) * map.pieces + piece, w);
     }
 }
 

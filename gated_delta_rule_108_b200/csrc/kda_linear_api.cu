@@ -25,19 +25,26 @@ bool supported_dim(int d) { return d == 64 || d == 128; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // How long the segments of a sequence of `chunks` chunks are, when `chains` CTAs work
-// on each segment number: the cheapest by the count of waves over the SMs.  In units
-// of one chunk of the chunk kernel (3.8 us at dk = dv = 128), as measured: a chunk of
-// the summing pass 0.5, a CTA 1.5 to start and end (1 there), its launch 2.
-int plan_segment_chunks(int64_t chains, int64_t chunks, double& best) {
+// on each segment number, and in how many pieces each is summed: the cheapest by the
+// count of waves over the SMs.  In units of one chunk of the chunk kernel (3.8 us at
+// dk = dv = 128), as measured: a chunk of the summing pass 0.5, a CTA 1.5 to start and
+// end (1 there), its launch 2.  Pieces only where no scan follows.  B=4, T=4096, H=16 (64
+// chains of 32 chunks, two segments): 106 us in one piece, 98 in two.
+int plan_segment_chunks(int64_t chains, int64_t chunks, double& best, int& pieces) {
     int64_t best_len = std::max<int64_t>(chunks, 1);
     best = 0;
+    pieces = 1;
     for (int64_t s = 1; s <= std::min<int64_t>(chunks, 96); ++s) {
         const int64_t len = (chunks + s - 1) / s, n = (chunks + len - 1) / len;
-        const double waves = std::ceil((double)(chains * n) / kSms), sums = std::ceil((double)(chains * (n - 1)) / kSms);
-        const double cost = waves * (len + 1.5) + (n > 1 ? sums * (0.5 * len + 1.0) + 2.0 : 0.0);
-        if (s == 1 || cost < best) {
-            best = cost;
-            best_len = len;
+        const double waves = std::ceil((double)(chains * n) / kSms);
+        for (int r = 1; r == 1 || (r <= len && n > 1 && (n - 1) * r < kLinDirect); ++r) {
+            const double sums = std::ceil((double)(chains * (n - 1) * r) / kSms);
+            const double cost = waves * (len + 1.5) + (n > 1 ? sums * (0.5 * std::ceil((double)len / r) + 1.0) + 2.0 : 0.0);
+            if ((s == 1 && r == 1) || cost < best) {
+                best = cost;
+                best_len = len;
+                pieces = r;
+            }
         }
     }
     return (int)best_len;
@@ -62,7 +69,7 @@ int plan_chained_chunks(int64_t chains, int64_t chunks, double& best) {
 }
 
 struct Plan {
-    int N, seg_tok, num_seg, max_segments, balance_tokens;
+    int N, seg_tok, num_seg, pieces, max_segments, balance_tokens;
     bool split, chained;
     size_t tab_off, seg_off, seg_bytes, total;   // seg_bytes: one role's segment states
     size_t flag_bytes;                           // chained: the flags, where packed batches have their table
@@ -79,25 +86,27 @@ bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, k
     const int64_t chunks = ((int64_t)T + kLinChunk - 1) / kLinChunk;
     const int64_t chains = per_head * H * (varlen ? 1 : std::max(B, 1));
     double cost = 0, cost_chained = 0;
-    int len = plan_segment_chunks(chains, chunks, cost);
+    int len = plan_segment_chunks(chains, chunks, cost, p.pieces);
     const int len_chained = (varlen || dtype != KDA_BF16) ? 0 : plan_chained_chunks(chains, chunks, cost_chained);
     p.chained = len_chained > 0 && cost_chained < 0.95 * cost;
     if (p.chained) len = len_chained;
     p.seg_tok = std::max(len, 1) * kLinChunk;
     p.num_seg = std::max<int>(1, (int)((chunks + len - 1) / std::max(len, 1)));
     p.split = p.num_seg > 1 && !p.chained;
+    // a sequence of a packed batch may have one segment more than the plan counts
+    if (!p.split || p.num_seg * p.pieces > kLinDirect) p.pieces = 1;
     // packed: every sequence may end in a short segment; unsplit when the longest is
     // within 1.75 times one SM's share.  H=16, cut and not: longest at 1.2 shares (of
     // 65,536 tokens in 15 sequences) 380 and 257 us, at 1.6 389 and 356, at 3 406 and 575
     const int64_t most = varlen ? (int64_t)p.N + T / p.seg_tok : (int64_t)p.N * p.num_seg;
-    if (most * H * per_head >= (int64_t)1 << 31) return false;
+    if (most * p.pieces * H * per_head >= (int64_t)1 << 31) return false;
     p.max_segments = (int)most;
     p.balance_tokens = (int)std::min<int64_t>((int64_t)1 << 30, (int64_t)(1.75 * (double)T * H * per_head / kSms));
     if (!p.split) p.balance_tokens = 1 << 30;
     p.tab_off = kHeaderBytes;
     p.flag_bytes = p.chained ? sizeof(int) * (size_t)p.max_segments * H * roles : 0;
     p.seg_off = round_up(p.tab_off + (varlen ? sizeof(int32_t) * (2 * (size_t)p.N + 2) : p.flag_bytes), 256);
-    p.seg_bytes = p.split || p.chained ? sizeof(float) * (size_t)p.max_segments * H * dk * dv : 0;
+    p.seg_bytes = p.split || p.chained ? sizeof(float) * (size_t)p.max_segments * p.pieces * H * dk * dv : 0;
     p.total = round_up(p.seg_off + p.seg_bytes * roles, 256);
     return true;
 }
@@ -152,7 +161,7 @@ LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, in
     a.bf16 = dtype == KDA_BF16;
     a.map.cu = cu;
     a.map.tab = cu ? reinterpret_cast<int32_t*>(ws + p.tab_off) : nullptr;
-    a.map.N = p.N; a.map.T = T; a.map.seg_tok = p.seg_tok; a.map.num_seg = p.num_seg;
+    a.map.N = p.N; a.map.T = T; a.map.seg_tok = p.seg_tok; a.map.num_seg = p.num_seg; a.map.pieces = 1;
     a.max_segments = p.max_segments;
     a.split = p.split;
     a.hdr = static_cast<WsHeader*>(workspace);
@@ -179,12 +188,13 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     auto pass = [&](bool states_only) { return all.bf16 ? launch_linear_tc(all, states_only) : launch_linear_simt(all, states_only); };
     all.reset = true;
     if (p.split && e == cudaSuccess) {
-        e = pass(true);
-        all.reset = false;
         // the most segments a sequence may have; and a state updated in place is read by the
         // scan, before the chunk kernel's last segments overwrite it
         all.scanned = (all.map.cu ? all.map.T / p.seg_tok + 1 : p.num_seg) > kLinDirect;
         for (int i = 0; i < all.roles; ++i) all.scanned |= all.role[i].s_in && all.role[i].s_in == all.role[i].s_out;
+        if (!all.scanned) all.map.pieces = p.pieces;
+        e = pass(true);
+        all.reset = false;
         if (e == cudaSuccess && all.scanned) e = launch_linear_scan(all);
     }
     return e == cudaSuccess ? pass(false) : e;

@@ -243,12 +243,12 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
     x /= args.slices;
     if (slice >= SL) return;                     // a role with fewer columns than another
     const LinRole& role = args.role[ri];
-    const int H = args.H, h = x % H, sidx = x / H;
+    const int H = args.H, h = x % H, slot = x / H, sidx = states_only ? slot / args.map.pieces : slot;
     if (sidx >= args.map.segments()) return;
-    const LinMap::Seg g = args.map.locate(sidx);
+    const LinMap::Seg g = states_only ? args.map.locate_piece(slot) : args.map.locate(sidx);
     const bool rev = role.reverse;
     const bool last = g.index == (rev ? 0 : g.count - 1);        // the segment processed last
-    if (states_only && last) return;
+    if (states_only && (last || g.len <= 0)) return;
     const int j0 = slice * kSimtCols;
     const int tid = threadIdx.x, lane = tid & 31, ty = tid >> 5, tx = lane >> 2, part = lane & 3;
     const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
@@ -257,7 +257,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
 
     const size_t zsize = (size_t)D1 * D2;
     const size_t user = ((size_t)g.seq * H + h) * zsize;
-    float* seg = role.seg ? role.seg + ((size_t)sidx * H + h) * zsize : nullptr;
+    float* seg = role.seg ? role.seg + ((size_t)slot * H + h) * zsize : nullptr;
     const float* pa = static_cast<const float*>(args.x[role.a]);
     const float* pb = static_cast<const float*>(args.x[role.b]);
     const float* pc = static_cast<const float*>(args.x[role.c]);
@@ -306,7 +306,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
                 z[n][m][2 * q + 1] = make_float2(v.z, v.w);
             }
     if (!states_only && !scanned)
-        lin_enter(g, sidx, rev, l, [&](int slot, float w) {
+        lin_enter(args.map, g, sidx, rev, l, [&](int slot, float w) {
             const float* own = role.seg + ((size_t)slot * H + h) * zsize;
 #pragma unroll
             for (int n = 0; n < HALVES; ++n)
@@ -492,7 +492,7 @@ cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
     static std::atomic<uint64_t> done;
     int only = states_only ? 1 : 0;
     void* args[] = {&b, &only};
-    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * a.H * a.roles * b.slices, 256, smem,
+    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * (states_only ? a.map.pieces : 1) * a.H * a.roles * b.slices, 256, smem,
                       args, a.stream, done);
 }
 

@@ -572,7 +572,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 }
                 if (!scanned && !args.chained)
-                    lin_enter(g, sidx, rev, l, [&](int slot, float w) {
+                    lin_enter(args.map, g, sidx, rev, l, [&](int slot, float w) {
                         float u[32];
                         read_columns<D1>(role.seg + ((size_t)slot * H + h) * zsize, row, j0, u);
 #pragma unroll
@@ -688,8 +688,8 @@ linear_tc_kernel(const __grid_constant__ LinTcParams prm)
 }
 
 // ----------------------------------------------------------- segment's sum --
-// Z of one segment from zero: sum_i lambda^{tokens from i to the segment's end}
-// b_i c_i^T.  The weights count to the segment's end, so nothing is rescaled.  Each
+// Z of one segment (or a piece of it) from zero: sum_i lambda^{tokens from i to its end}
+// b_i c_i^T.  The weights count to that end, so nothing is rescaled.  Each
 // chunk's sum is formed in TMEM (two of them, in turn) and added in registers, 32
 // elements a thread: the tensor core's cut-off sums would pile up over a long
 // segment.  Half a chunk of c is weighted, by sixteen warps, while the other half is
@@ -721,11 +721,12 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     const LinArgs& args = prm.a;
     const LinRole& role = args.role[ri];
     const int x = blockIdx.x / args.roles;
-    const int H = args.H, h = x % H, sidx = x / H;
-    if (sidx >= args.map.segments()) return;
-    const LinMap::Seg g = args.map.locate(sidx);
+    const int H = args.H, h = x % H, slot = x / H;
+    if (slot >= args.map.segments() * args.map.pieces) return;
+    const LinMap::Seg g = args.map.locate_piece(slot);
     const bool rev = role.reverse;
     if (g.index == (rev ? 0 : g.count - 1)) return;     // processed last: its sum enters no other segment
+    if (g.len <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = role.s_out ? 3 : 2;
     const float c_upd = role.c_upd;
@@ -840,7 +841,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
         }
         if (ok) ok = add(nch - 1);
         if (ok && (D1 == 128 || quad < 2)) {
-            float* to = role.seg + ((size_t)sidx * H + h) * D1 * D2 + (size_t)COLS * sub * D1 + row;
+            float* to = role.seg + ((size_t)slot * H + h) * D1 * D2 + (size_t)COLS * sub * D1 + row;
 #pragma unroll
             for (int j = 0; j < COLS; ++j) to[(size_t)j * D1] = z[j];
         }
@@ -870,7 +871,7 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     const int smem = (int)(states_only ? sum : chunk) + 1024;
     static std::atomic<uint64_t> done[2];
     void* args[] = {const_cast<LinTcParams*>(&p)};
-    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * a.H * a.roles,
+    return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * (states_only ? a.map.pieces : 1) * a.H * a.roles,
                       states_only ? kLinSumThreads : kLinThreads, smem, args, a.stream, done[states_only]);
 }
 

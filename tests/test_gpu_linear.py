@@ -353,6 +353,22 @@ def test_many_short_sequences(cuda_device):
         check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
 
 
+@pytest.mark.parametrize("T,H,dk,dv,dtype,lens", [(1500, 60, 64, 64, torch.bfloat16, None), (1409, 60, 64, 64, torch.bfloat16, None),
+                                                  (1500, 60, 64, 64, torch.float32, None), (1500, 30, 64, 128, torch.float32, None),
+                                                  (1700, 60, 64, 64, torch.bfloat16, (1600, 0, 100))], ids=str)
+@pytest.mark.parametrize("decay", ["slopes", "strong", "none"])
+def test_segments_summed_in_pieces(cuda_device, T, H, dk, dv, dtype, lens, decay):
+    """60 chains (20 heads for the gradients): two segments, the sum in two pieces; packed, one of the batch's three is cut."""
+    N = 1 if lens is None else len(lens)
+    slots = lambda size: (size - 256) / (H * dk * dv * 4)  # noqa: E731
+    assert slots(kda.linear_chunk_fwd_workspace_size(1, T, H, dk, dv, N, lens is not None, dtype)) >= 4
+    x, _ = case(1, T, H, dk, dv, dtype, decay=decay, lens=lens, seed=25)
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    check_fwd(x, o, S)
+    x, back = case(1, T, H // 3, dk, dv, dtype, decay=decay, lens=lens, seed=26)
+    check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
+
+
 def test_offsets_past_31_bits(cuda_device):
     """q, k, v and o of more than 2^31 elements each: the short sequence behind the long one, and the norm there."""
     lens, H, d = (524300, 200), 32, 128
