@@ -310,6 +310,23 @@ def test_side_stream_and_graph(cuda_device, B, T, H, dtype):
         assert all(torch.equal(gg[n], ge[n]) for n in gg)
 
 
+def test_more_than_32_sequences(cuda_device):
+    """A long one among 40 short: ordered, cut and checked by the whole block."""
+    lens = [30 + i for i in range(20)] + [3000] + [0, 1] + [50 - i for i in range(18)]
+    x, back = case(1, sum(lens), 1, 64, 64, torch.bfloat16, lens=lens, seed=27)
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    check_fwd(x, o, S)
+    check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
+    d = dev(x)
+    for at, value in ((0, 1), (41, sum(lens) + 1), (7, 2 ** 31 - 1), (9, -5), (30, 2000)):
+        cu = x["cu_seqlens"].clone()
+        cu[at] = value
+        o, S = torch.full_like(o, 7.0), torch.full_like(S, 7.0)
+        with pytest.raises(kda.KDAError, match="BAD_SEQLENS"):
+            kda.linear_chunk_fwd(**{**d, "cu_seqlens": cu.cuda()}, o=o, final_state=S, check=True)
+        assert bool((o == 7).all()) and bool((S == 7).all())
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 def test_two_streams_at_once(cuda_device, dtype):
     """Calls that overlap, each with its own workspace."""
