@@ -136,14 +136,17 @@ struct LinArgs {
     WsHeader* hdr;                // null where a call needs no more workspace than this and the caller gave none
     long long wait_cap;           // test hook: cycles after which a wait gives up, one copy left out (0: neither)
     bool reset;                   // the launch starts the call: block 0 clears the status
+    bool follows;                 // another kernel of the call comes before this launch
     cudaStream_t stream;
 };
 
-// What every kernel of a call begins with: true where the call goes on.  The
+// What every kernel of a call begins with, before it reads or writes anything that
+// another kernel of the call touches: true where the call goes on.  The
 // segment table's kernel has left the status of a packed batch; otherwise the first
 // launch clears it (block 0 is among the first to run, and another block records an
 // error only after a wait of a second).
 __device__ __forceinline__ bool lin_begin(const LinArgs& a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");    // the kernel of this call before this one has ended
     if (a.map.cu) return a.hdr->status == kStatusOk;
     if (a.reset && a.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
         a.hdr->status = kStatusOk;
@@ -191,22 +194,35 @@ __device__ __forceinline__ int lin_skip(double l, int len, int chunk, int chunks
 // Launches a kernel with more shared memory than every kernel may have.  It is allowed
 // that on the current device once (`done` holds a bit for each device, above 64 every
 // call asks), and again if this launch itself is refused, as after a reset of the
-// device; an error that an earlier call has left says nothing about this one.
+// device; an error that an earlier call has left says nothing about this one.  With
+// `follows` the blocks may start while the kernel before, of the same call, ends; they
+// wait for it in lin_begin.  T=2048, H=8: 25.7 us without, 24.6 with; five packed
+// sequences 25.2 and 24.2.
 inline cudaError_t lin_launch(const void* kernel, size_t grid, int threads, int smem_bytes, void** args,
-                              cudaStream_t stream, std::atomic<uint64_t>& done) {
+                              bool follows, cudaStream_t stream, std::atomic<uint64_t>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    cudaLaunchAttribute after{};
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem_bytes;
+    c.stream = stream;
+    c.attrs = &after;
+    c.numAttrs = follows ? 1 : 0;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) {
-        e = cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem_bytes, stream);
+        e = cudaLaunchKernelExC(&c, kernel, args);
         if (e != cudaErrorInvalidValue) return e;
         cudaGetLastError();
     }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
-    return cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(threads), args, smem_bytes, stream);
+    return cudaLaunchKernelExC(&c, kernel, args);
 }
 
 cudaError_t launch_linear_prep(const LinArgs& a, int32_t* tab, int seg_tok, int balance_tokens);

@@ -187,6 +187,7 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
     }
     auto pass = [&](bool states_only) { return all.bf16 ? launch_linear_tc(all, states_only) : launch_linear_simt(all, states_only); };
     all.reset = true;
+    all.follows = all.map.cu != nullptr;
     if (p.split && e == cudaSuccess) {
         // the most segments a sequence may have; and a state updated in place is read by the
         // scan, before the chunk kernel's last segments overwrite it
@@ -195,6 +196,7 @@ cudaError_t run_roles(const LinArgs& a, const Plan& p, char* ws) {
         if (!all.scanned) all.map.pieces = p.pieces;
         e = pass(true);
         all.reset = false;
+        all.follows = true;
         if (e == cudaSuccess && all.scanned) e = launch_linear_scan(all);
     }
     return e == cudaSuccess ? pass(false) : e;

@@ -530,7 +530,7 @@ cudaError_t launch_simt_t(const LinArgs& a, bool states_only) {
     int only = states_only ? 1 : 0;
     void* args[] = {&b, &only};
     return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * (states_only ? a.map.pieces : 1) * a.H * a.roles * b.slices, 256, smem,
-                      args, a.stream, done);
+                      args, a.follows, a.stream, done);
 }
 
 }  // namespace

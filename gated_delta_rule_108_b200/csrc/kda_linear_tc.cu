@@ -872,7 +872,7 @@ cudaError_t launch_tc_t(const LinTcParams& p, bool states_only) {
     static std::atomic<uint64_t> done[2];
     void* args[] = {const_cast<LinTcParams*>(&p)};
     return lin_launch(reinterpret_cast<const void*>(kern), (size_t)a.max_segments * (states_only ? a.map.pieces : 1) * a.H * a.roles,
-                      states_only ? kLinSumThreads : kLinThreads, smem, args, a.stream, done[states_only]);
+                      states_only ? kLinSumThreads : kLinThreads, smem, args, a.follows, a.stream, done[states_only]);
 }
 
 }  // namespace
