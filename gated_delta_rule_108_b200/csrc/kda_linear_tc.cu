@@ -13,12 +13,14 @@
 // first.  Four products of 128-row tiles, all kind::f16 with bf16 operands and fp32
 // accumulators in TMEM; a, b and c are exact in bf16, so only P, Z and the
 // weighted c are rounded:
-//  - P in two bf16 parts (2^-17), the A operand in TMEM, in place of its fp32 values
-//    (one part would save 0.2 us of 4.5 us a chunk and bring o's error from 1.2 to 1.4
-//    times its own rounding);
-//  - Z in one part as operand: it only reaches y, itself bf16, and adds at most its
-//    own rounding to y's; the state itself stays fp32 in TMEM;
-//  - the weighted c in three parts (2^-25) where the state is a result, in two where
+//  - P in two bf16 parts (2^-16), the A operand in TMEM, in place of its fp32 values;
+//  - Z in two parts (2^-16) as operand, one after the other; the state itself stays
+//    fp32 in TMEM.  y's own rounding is no measure for it: a row of a may read Z from
+//    a direction in which Z holds little, and what a part leaves out scales with
+//    |Z| |a|, not with y (one part, and keys within 0.1 of a direction that the queries
+//    are orthogonal to: o off by ten times its rounding).  The second part costs 6 to
+//    12 % of a forward;
+//  - the weighted c in three parts (2^-24) where the state is a result, in two where
 //    it only reaches y: a state is a sum over the whole sequence, and fp32 is what
 //    it is returned in (two parts everywhere would save 0.4 us of 4.5 us a chunk).
 // The tensor core cuts its sums off instead of rounding them, always towards zero.
@@ -29,8 +31,8 @@
 // One CTA per (segment, head, role), one per SM: 512 columns of TMEM hold Z, U, P and
 // y.  Warp 17 loads tiles by TMA, warp 16 issues the MMAs, warps 0-7 weight P and y's
 // rows of Z^T a, weight the last quarter of c and take y out, warps 8-15 keep Z, write
-// its operand and weight the other quarters.  The chain from chunk to chunk (Z ->
-// operand -> Z^T a, U) and the rest overlap: b and c have two buffers each, so the next
+// its operands and weight the other quarters.  The chain from chunk to chunk (Z ->
+// operands -> Z^T a, U) and the rest overlap: b and c have two buffers each, so the next
 // chunk's tiles are in flight while this one is worked on; a's buffer frees as soon as
 // P and Z^T a are done; y leaves through the buffer of its own chunk's c (warp 18 sends
 // it out by TMA; stored straight from registers a chunk takes 5.2 us instead of 4.6).
@@ -256,13 +258,15 @@ struct LinSmem {
     static constexpr uint32_t A = 0;
     static constexpr uint32_t B = A + AT;                        // b of two chunks
     static constexpr uint32_t CC = B + 2 * AT;                   // c of two chunks; y leaves through its own chunk's
-    static constexpr uint32_t Z = CC + 2 * CT;                   // bf16 Z: D2 / 64 tiles of D1 rows
-    // Weighted c of one step, three parts: steps 0 and 1 have a place of their own, 2 and
-    // 3 take that of Z's operand, which nothing reads after a Z.
+    // Two places that Z's operand and the weighted c share in turn: bf16 Z, D2 / 64 tiles
+    // of D1 rows a part, or the weighted c of one step, three parts.  The second place
+    // holds step 0, then Z's second part, then step 2; the first Z's first part, then
+    // steps 1 and 3.
     static constexpr uint32_t CWB = 3 * (D2 / 64) * kLinStep * 128;
     static constexpr uint32_t ZB = (D2 / 64) * D1 * 128 > CWB ? (D2 / 64) * D1 * 128 : CWB;
+    static constexpr uint32_t Z = CC + 2 * CT;
     static constexpr uint32_t CW = Z + ZB;
-    static constexpr uint32_t END = CW + CWB;
+    static constexpr uint32_t END = CW + ZB;
     static_assert(END + 1024 + 1200 <= 232448, "shared memory");
     static_assert(ZB >= D1 / 16 * 2048, "a state's way through Z's place");
 };
@@ -276,7 +280,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t full_a, az_done, full_b[2], empty_b[2], full_c[2], empty_c[2], p_done, p_ready,
-        y_done, y_free, y_staged[2], cw_ready[2], cw_free[2], upd_done, z_ready, drained;
+        y_done, y_free, y_staged[2], cw_ready[2], cw_free[2], upd_done, z_ready, zh_done, zl_ready, drained;
     __shared__ uint32_t s_tmem;
     __shared__ LinWait s_wait;
     __shared__ float pw[C + 1];
@@ -318,6 +322,8 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         }
         mbar_init(&upd_done, 1);
         mbar_init(&z_ready, 256);
+        mbar_init(&zh_done, 1);
+        mbar_init(&zl_ready, 256);
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
@@ -396,6 +402,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         // descriptors: K-major a, b; MN-major b (the update's A), Z, c, weighted c in its two places
         const uint64_t a_k = smem_desc(smem_u32(sm + Sm::A), 16, 1024, kLayoutSW128);
         const uint64_t z_mn = smem_desc(smem_u32(sm + Sm::Z), D1 * 128, 1024, kLayoutSW128);
+        const uint64_t zl_mn = smem_desc(smem_u32(sm + Sm::CW), D1 * 128, 1024, kLayoutSW128);
         const uint64_t w_mn0 = smem_desc(smem_u32(sm + Sm::CW), kLinStep * 128, 1024, kLayoutSW128);
         const uint64_t w_mn1 = smem_desc(smem_u32(sm + Sm::Z), kLinStep * 128, 1024, kLayoutSW128);
         const uint64_t b_k0 = smem_desc(smem_u32(sm + Sm::B), 16, 1024, kLayoutSW128);
@@ -422,21 +429,31 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
             // U = b^T (weighted c) in four steps, as their operands come; between them y = a Z and,
             // on top of its weighted rows, y += P c
             auto update = [&](int i) {
-                const bool ok = lin_wait_warp(&cw_ready[i >> 1], i & 1, &s_wait);
+                const bool ok = lin_wait_warp(&cw_ready[i & 1], i >> 1, &s_wait);
                 tc_fence_after();
                 if (ok && elect_one()) {
-                    issue_update<D2, kLinStep>(UACC, b_mn, i < 2 ? w_mn0 : w_mn1, kLinStep * i, parts, i == 0);
-                    mma_commit(&cw_free[i >> 1]);
+                    issue_update<D2, kLinStep>(UACC, b_mn, i & 1 ? w_mn1 : w_mn0, kLinStep * i, parts, i == 0);
+                    mma_commit(&cw_free[i & 1]);
                 }
                 return ok;
             };
             if (!lin_wait_warp(&z_ready, ph, &s_wait) || !update(0)) break;
             if (n > 0 && !lin_wait_warp(&y_free, prev, &s_wait)) break;
             tc_fence_after();
-            if (elect_one()) {
+            // y = a Z: Z's first part, then its second, which comes where step 0 was
+            auto read_z = [&](uint64_t z, bool first) {
 #pragma unroll
                 for (int k = 0; k < D1 / 16; ++k)
-                    mma_f16(YACC, desc_at(a_k, (k >> 2) * kTile + (k & 3) * 32), desc_at(z_mn, k * 2048), id_y, k != 0);
+                    mma_f16(YACC, desc_at(a_k, (k >> 2) * kTile + (k & 3) * 32), desc_at(z, k * 2048), id_y, !(first && k == 0));
+            };
+            if (elect_one()) {
+                read_z(z_mn, true);
+                mma_commit(&zh_done);
+            }
+            if (!lin_wait_warp(&zl_ready, ph, &s_wait)) break;
+            tc_fence_after();
+            if (elect_one()) {
+                read_z(zl_mn, false);
                 mma_commit(&az_done);
             }
             if (!update(1) || !update(2) || !lin_wait_warp(&p_ready, ph, &s_wait)) break;
@@ -593,46 +610,69 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
             }
 #pragma unroll 1
             for (int i = 0; i < 3; ++i) {
-                if (i == 1) {       // step 0 is ahead of Z, while the previous chunk's update runs
-                    if (n > 0) ok = lin_wait_warp(&upd_done, (n - 1) & 1, &s_wait);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (mine) {                         // Z <- lambda^L Z + U of the previous chunk; its bf16 operand
-                        const float gam = n > 0 ? pw[len_before] : 1.f;
-#pragma unroll 1
-                        for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
-                            float v[32], u[32];
-                            tmem_ld32x2_sync(ZREG + lane_base + j0, UACC + lane_base + j0, v, u);
-                            if (n > 0) {
-                                uint32_t d[32];
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    const float2 x = fma2(make_float2(gam, gam), make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
-                                    v[j] = x.x; v[j + 1] = x.y;
-                                    d[j] = __float_as_uint(x.x);
-                                    d[j + 1] = __float_as_uint(x.y);
-                                }
-                                tmem_st32(ZREG + lane_base + j0, d);
-                            }
-#pragma unroll
-                            for (int j8 = 0; j8 < 4; ++j8)
-                                *reinterpret_cast<uint4*>(sm + Sm::Z + (j0 >> 6) * (D1 * 128) + sw128_offset(row, 64 * sub + 16 * j8)) =
-                                    make_uint4(pack_bf16(v[8 * j8], v[8 * j8 + 1]), pack_bf16(v[8 * j8 + 2], v[8 * j8 + 3]),
-                                               pack_bf16(v[8 * j8 + 4], v[8 * j8 + 5]), pack_bf16(v[8 * j8 + 6], v[8 * j8 + 7]));
-                        }
-                        tmem_wait_st();
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    mbar_arrive(&z_ready);
-                }
-                // the step's place is free: of the step before, or (step 2) of Z's operand
-                if (i == 2) ok = lin_wait_warp(&az_done, n & 1, &s_wait);
-                else if (n > 0 || i == 1) ok = lin_wait_warp(&cw_free[0], i == 0, &s_wait);
+                // the step's place is free: of the step or the part of Z before
+                if (i == 0) ok = n == 0 || lin_wait_warp(&cw_free[0], 1, &s_wait);
+                else ok = lin_wait_warp(i == 1 ? &zh_done : &az_done, n & 1, &s_wait);
                 if (!ok) break;
-                weight_c<D2, kLinStep>(buf_c(n), sm + (i < 2 ? Sm::CW : Sm::Z), kLinStep * i, parts, L, pw, c_upd, rev, t);
+                weight_c<D2, kLinStep>(buf_c(n), sm + (i & 1 ? Sm::Z : Sm::CW), kLinStep * i, parts, L, pw, c_upd, rev, t);
                 fence_proxy_async_smem();
-                mbar_arrive(&cw_ready[i >> 1]);
+                mbar_arrive(&cw_ready[i & 1]);
+                if (i > 0) continue;
+
+                // Z, while the others wait for it: step 0 was ahead, during the previous chunk's update
+                if (n > 0) ok = lin_wait_warp(&upd_done, (n - 1) & 1, &s_wait);
+                if (!ok) break;
+                tc_fence_after();
+                if (mine) {                             // Z <- lambda^L Z + U of the previous chunk; its operand's first part
+                    const float gam = n > 0 ? pw[len_before] : 1.f;
+#pragma unroll 1
+                    for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
+                        float v[32], u[32];
+                        tmem_ld32x2_sync(ZREG + lane_base + j0, UACC + lane_base + j0, v, u);
+                        if (n > 0) {
+                            uint32_t d[32];
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 x = fma2(make_float2(gam, gam), make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
+                                v[j] = x.x; v[j + 1] = x.y;
+                                d[j] = __float_as_uint(x.x);
+                                d[j + 1] = __float_as_uint(x.y);
+                            }
+                            tmem_st32(ZREG + lane_base + j0, d);
+                        }
+#pragma unroll
+                        for (int j8 = 0; j8 < 4; ++j8)
+                            *reinterpret_cast<uint4*>(sm + Sm::Z + (j0 >> 6) * (D1 * 128) + sw128_offset(row, 64 * sub + 16 * j8)) =
+                                make_uint4(pack_bf16(v[8 * j8], v[8 * j8 + 1]), pack_bf16(v[8 * j8 + 2], v[8 * j8 + 3]),
+                                           pack_bf16(v[8 * j8 + 4], v[8 * j8 + 5]), pack_bf16(v[8 * j8 + 6], v[8 * j8 + 7]));
+                    }
+                    tmem_wait_st();
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&z_ready);
+
+                ok = lin_wait_warp(&cw_free[0], 0, &s_wait);
+                if (!ok) break;
+                if (mine) {                             // what the first part has left of Z
+#pragma unroll 1
+                    for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
+                        float v[32];
+                        uint32_t p[16];
+                        tmem_ld32_sync(ZREG + lane_base + j0, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 x = rest_of(make_float2(v[2 * j], v[2 * j + 1]), pack_bf16(v[2 * j], v[2 * j + 1]));
+                            p[j] = pack_bf16(x.x, x.y);
+                        }
+#pragma unroll
+                        for (int j8 = 0; j8 < 4; ++j8)
+                            *reinterpret_cast<uint4*>(sm + Sm::CW + (j0 >> 6) * (D1 * 128) + sw128_offset(row, 64 * sub + 16 * j8)) =
+                                make_uint4(p[4 * j8], p[4 * j8 + 1], p[4 * j8 + 2], p[4 * j8 + 3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&zl_ready);
             }
         }
         if (ok && nch > 0) ok = lin_wait_warp(&upd_done, (nch - 1) & 1, &s_wait);

@@ -359,9 +359,12 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
  * after another instead and nothing is summed twice.  B*T < 2^30.
  *
  * Numerics: bf16 inputs use the tensor cores with bf16 operands and fp32
- * accumulation; o differs from the exact result by about 1.4 times its own
- * rounding at most, and the states keep fp32 (the factors that enter them are
- * split into three bf16 parts).  fp32 inputs are computed in fp32 on CUDA cores.
+ * accumulation; what is rounded on the way (the weighted products <q_t, k_i>, the
+ * state that a chunk starts from) enters in two bf16 parts.  o is off by its own
+ * rounding and by up to 2^-14 of the sum of the magnitudes it is made of, which
+ * shows where that sum nearly cancels.  The states keep fp32 (the factors that
+ * enter them are split into three bf16 parts).  fp32 inputs are computed in fp32 on
+ * CUDA cores.
  * Inputs must be finite: an infinity or a NaN at one token reaches every output
  * of its chunk of 128 tokens, also those before it.  It does not reach other
  * sequences.

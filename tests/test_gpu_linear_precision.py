@@ -1,0 +1,67 @@
+"""How exact the linear attention with one decay per head is, where the tests of its
+results leave room: outputs that cancel against what they are summed from, states and
+fp32 results in 2-norm, sums over a long sequence."""
+import pytest
+import torch
+
+import linear_plain as P
+from gated_delta_rule_108_b200 import kda
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(x):
+    return {n: None if t is None else t.cuda() for n, t in x.items()}
+
+
+def along(g, B, T, H, d, axis, c):
+    """Unit rows around one channel pattern: `axis` (+1 or -1) names one of two orthogonal ones."""
+    base = torch.ones(d)
+    base[d // 2:] = axis
+    x = base * d ** -0.5 + c * torch.randn(B, T, H, d, generator=g) * d ** -0.5
+    return (x / x.norm(dim=-1, keepdim=True)).bfloat16()
+
+
+def cancelling(B, T, H, dk, dv, c, decay, lens=None, seed=0):
+    """Keys and queries around orthogonal directions, values and cotangents likewise: every
+    output reads a state from a direction in which it holds little."""
+    g = torch.Generator().manual_seed(seed)
+    N = B if lens is None else len(lens)
+    l = None if decay is None else torch.full((H,), decay)
+    row = lambda d, axis: torch.cat((torch.ones(d // 2), axis * torch.ones(d - d // 2))) * d ** -0.5  # noqa: E731
+    S0 = (8 * row(dk, 1)[:, None] * row(dv, 1)[None]).expand(N, H, dk, dv) + 0.01 * torch.randn(N, H, dk, dv, generator=g)
+    dS = (8 * row(dk, -1)[:, None] * row(dv, -1)[None]).expand(N, H, dk, dv) + 0.01 * torch.randn(N, H, dk, dv, generator=g)
+    x = dict(q=along(g, B, T, H, dk, -1, c), k=along(g, B, T, H, dk, 1, c), v=along(g, B, T, H, dv, 1, c), log_decay=l,
+             initial_state=S0.contiguous(),
+             cu_seqlens=None if lens is None else torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32))
+    return x, dict(d_o=along(g, B, T, H, dv, -1, c), d_final_state=dS.contiguous())
+
+
+def check_output(x, ref, mag, what, tokens):
+    """bf16 outputs: their own rounding, and of the magnitudes summed what two bf16 parts of
+    P, of the state and of the update's operand leave out, 2^-16 each, besides the fp32 sums'
+    part (see linear_plain.assert_close)."""
+    x, ref, mag = x.double().cpu(), ref.double(), mag.double()
+    n = 2 * (300 + 24 * -(-tokens // 128)) * 2.0 ** -24 + 2.0 ** -22
+    tol = (2.0 ** -8 + 2.0 ** -14) * ref.abs() + (3 * 2.0 ** -16 + n) * mag
+    bad = ~((x - ref).abs() <= tol)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} beyond the bound, first at {bad.nonzero()[0].tolist()}, "
+                           f"relative error {float((x - ref).norm() / ref.norm()):.2e}")
+
+
+@pytest.mark.parametrize("c", [1.0, 0.3, 0.1])
+@pytest.mark.parametrize("B,T,H,dk,dv,decay,lens", [
+    (1, 300, 2, 128, 128, None, None), (2, 129, 1, 64, 64, -0.01, None), (1, 200, 2, 128, 64, None, None),
+    (1, 260, 2, 64, 128, -0.001, None), (1, 1500, 1, 128, 128, None, None), (1, 3000, 1, 64, 64, -0.0005, None),
+    (1, 700, 1, 128, 128, None, (1, 420, 0, 279))], ids=str)
+def test_reads_that_cancel(cuda_device, B, T, H, dk, dv, decay, lens, c):
+    x, back = cancelling(B, T, H, dk, dv, c, decay, lens, seed=T)
+    longest = max(P.lens_of(B, T, x["cu_seqlens"]))
+    ref, _, om, _ = P.forward(x["q"], x["k"], x["v"], x["log_decay"], x["initial_state"], x["cu_seqlens"])
+    o, _ = kda.linear_chunk_fwd(**dev(x), check=True)
+    check_output(o, ref, om, "o", longest)
+    g, m = P.backward(x["q"], x["k"], x["v"], x["log_decay"], back["d_o"], x["initial_state"], back["d_final_state"],
+                      x["cu_seqlens"])
+    r = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
+    for n in ("dq", "dk", "dv"):
+        check_output(r[n], g[n], m[n], n, longest)
