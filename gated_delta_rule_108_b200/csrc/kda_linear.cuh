@@ -45,6 +45,7 @@ struct LinRole {
     bool reverse;           // from the last token to the first
     float c_inter, c_intra; // y_t = c_inter lambda^.. Z_0^T a_t + c_intra sum_i lambda^.. <a_t, b_i> c_i
     float c_upd;
+    int parts;              // bf16 parts of the weighted c; the role decides, so that no output depends on another being asked for
 };
 
 // Where the segments lie.  Sequences are B rows of T tokens, or packed by cu.

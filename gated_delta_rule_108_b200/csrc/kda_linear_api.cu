@@ -252,7 +252,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
         a.wait_cap = g_drop_cap;
         g_drop_cap = 0;
     }
-    a.role[0] = {0, 1, 2, o, initial_state, final_state, nullptr, false, false, s, s, 1.f};
+    a.role[0] = {0, 1, 2, o, initial_state, final_state, nullptr, false, false, s, s, 1.f, 3};
     const cudaError_t e = run_roles(a, p, static_cast<char*>(workspace));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_chunk_fwd launch failed: %s", cudaGetErrorString(e));
     return fail(KDA_OK, "");
@@ -295,9 +295,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
     for (int i = 0; i < 4; ++i) { a.x[i] = x[i]; a.dim[i] = dims[i]; }
     const float s = 1.0f / sqrtf((float)dk);
     a.roles = 3;
-    a.role[0] = {3, 2, 1, dq, initial_state, nullptr, nullptr, true, false, s, s, 1.f};
-    a.role[1] = {2, 3, 0, dk_out, d_final_state, nullptr, nullptr, true, true, 1.f, s, s};
-    a.role[2] = {1, 0, 3, dv_out, d_final_state, d_initial_state, nullptr, false, true, 1.f, s, s};
+    a.role[0] = {3, 2, 1, dq, initial_state, nullptr, nullptr, true, false, s, s, 1.f, 2};
+    a.role[1] = {2, 3, 0, dk_out, d_final_state, nullptr, nullptr, true, true, 1.f, s, s, 2};
+    a.role[2] = {1, 0, 3, dv_out, d_final_state, d_initial_state, nullptr, false, true, 1.f, s, s, 3};
     const cudaError_t e = run_roles(a, p, static_cast<char*>(workspace));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "kda_linear_chunk_bwd launch failed: %s", cudaGetErrorString(e));
     return fail(KDA_OK, "");

@@ -20,8 +20,8 @@
 //    |Z| |a|, not with y (one part, and keys within 0.1 of a direction that the queries
 //    are orthogonal to: o off by ten times its rounding).  The second part costs 6 to
 //    12 % of a forward;
-//  - the weighted c in three parts (2^-24) where the state is a result, in two where
-//    it only reaches y: a state is a sum over the whole sequence, and fp32 is what
+//  - the weighted c in three parts (2^-24) in the roles whose state is a result (of the
+//    forward, of dv), in two where it only reaches y: a state is a sum over the whole sequence, and fp32 is what
 //    it is returned in (two parts everywhere would save 0.4 us of 4.5 us a chunk).
 // The tensor core cuts its sums off instead of rounding them, always towards zero.
 // So each chunk's sum U starts from zero and is added to Z in registers, rounded:
@@ -297,7 +297,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
     const int nch = (g.len + C - 1) / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t zsize = (size_t)D1 * D2, user = ((size_t)g.seq * H + h) * zsize;
-    const int parts = role.s_out ? 3 : 2;
+    const int parts = role.parts;
     // in registers: the asm statements below make the compiler read memory again
     const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
     __nv_bfloat16* const yout = static_cast<__nv_bfloat16*>(role.y);
@@ -768,7 +768,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
     if (g.index == (rev ? 0 : g.count - 1)) return;     // processed last: its sum enters no other segment
     if (g.len <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int parts = role.s_out ? 3 : 2;
+    const int parts = role.parts;
     const float c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
     const int chunks = (g.len + C - 1) / C, skip = lin_skip(l, g.len, C, chunks, rev), nch = chunks - skip;

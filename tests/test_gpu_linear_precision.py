@@ -65,3 +65,21 @@ def test_reads_that_cancel(cuda_device, B, T, H, dk, dv, decay, lens, c):
     r = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
     for n in ("dq", "dk", "dv"):
         check_output(r[n], g[n], m[n], n, longest)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("B,T,H,lens", [(2, 300, 2, None), (1, 3000, 1, None), (1, 1500, 60, None), (5, 2048, 32, None),
+                                        (1, 700, 1, (1, 420, 0, 279))], ids=str)
+def test_no_output_depends_on_another_being_asked_for(cuda_device, B, T, H, lens, dtype):
+    """One segment, many, some summed in pieces, some that follow one another, packed."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    d = 64 if H > 2 else 128
+    q, k, v, d_o = (torch.randn(B, T, H, d, generator=g, device="cuda").to(dtype) for _ in range(4))
+    l = -torch.rand(H, generator=g, device="cuda")
+    cu = None if lens is None else torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    o, S = kda.linear_chunk_fwd(q, k, v, l, cu_seqlens=cu)
+    alone, none = kda.linear_chunk_fwd(q, k, v, l, cu_seqlens=cu, output_final_state=False)
+    assert none is None and torch.equal(o, alone)
+    full = kda.linear_chunk_bwd(q, k, v, l, d_o, cu_seqlens=cu)
+    r = kda.linear_chunk_bwd(q, k, v, l, d_o, cu_seqlens=cu, output_d_initial_state=False)
+    assert r["dS0"] is None and all(torch.equal(r[n], full[n]) for n in ("dq", "dk", "dv"))
