@@ -25,13 +25,20 @@ cudaError_t mark_stage(int i, cudaStream_t s) {
     return i < g_stage_event_count ? cudaEventRecord(g_stage_events[i], s) : cudaSuccess;
 }
 
-kda_status fail(kda_status st, const char* fmt, ...) {
+// The runtime keeps a failed call's error for this thread's next cudaGetLastError, which
+// would take it for its own launch's: it ends with the call that reports it.
+void record(int st, const char* fmt, va_list ap) {
     char buf[512];
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    g_last_error = buf;
+    if (st == KDA_ERR_CUDA) (void)cudaGetLastError();
+}
+
+kda_status fail(kda_status st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    record(st, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return st;
 }
 
@@ -157,12 +164,10 @@ int chunk_fwd_fused(int N, bool varlen, kda_dtype dtype, const WsLayout& L, size
 
 namespace kda {
 int set_error(int status, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    record(status, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return status;
 }
 }  // namespace kda
