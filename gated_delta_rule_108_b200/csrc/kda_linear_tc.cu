@@ -224,7 +224,10 @@ __device__ __forceinline__ void write_rows(float* s, unsigned char* stage, int r
 }
 
 // A state handed from one block to a later one: each warp counts itself in once its
-// part is written; every warp of the reader waits for all of them.
+// part is written; every warp of the reader waits for all of them.  A block that has
+// given up says so in the same word, and the blocks after it pass that on without a
+// wait of their own: else a chain could hold the GPU for one bounded wait a segment.
+constexpr int kLinFailed = 1 << 30;
 __device__ __forceinline__ void raise_flag(int* flag) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
@@ -237,8 +240,9 @@ __device__ __forceinline__ bool wait_flag(const int* flag, int count, LinWait* w
     int seen;
     do {
         asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+        if (seen >= kLinFailed) seen = -1;
         if (seen < count) {
-            if (*(volatile int*)&w->abort || clock64() - t0 > w->cap) {
+            if (seen < 0 || *(volatile int*)&w->abort || clock64() - t0 > w->cap) {
                 *(volatile int*)&w->abort = 1;
                 break;
             }
@@ -298,6 +302,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t zsize = (size_t)D1 * D2, user = ((size_t)g.seq * H + h) * zsize;
     const int parts = role.parts;
+    int* const flag = args.chained ? args.flags + ((size_t)sidx * H + h) * args.roles + ri : nullptr;
     // in registers: the asm statements below make the compiler read memory again
     const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
     __nv_bfloat16* const yout = static_cast<__nv_bfloat16*>(role.y);
@@ -372,7 +377,8 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                 load_tile<D2>(buf_c(n), &prm.map[role.c], &full_c[i], h, tok);
                 ++nc;
                 if (n > 0 && !lin_wait(&az_done, (n - 1) & 1, &s_wait)) break;
-                if (args.wait_cap > 0 && blockIdx.x == 0 && n == min(2, nch - 1)) continue;   // the test hook's missing copy
+                // the test hook's missing copy
+                if (args.wait_cap > 0 && (args.chained ? g.index == 0 : blockIdx.x == 0) && n == min(2, nch - 1)) continue;
                 load_tile<D1>(sm + Sm::A, &prm.map[role.a], &full_a, h, tok);
                 ++na;
             }
@@ -572,7 +578,10 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
             const bool scanned = args.scanned && g.count > 1;
             const int before = sidx + (rev ? 1 : -1);           // the segment processed before this one
             const bool chained = args.chained && g.index != (rev ? g.count - 1 : 0);
-            if (chained) ok = wait_flag(args.flags + ((size_t)before * H + h) * args.roles + ri, D1 / 16, &s_wait);
+            if (chained) {
+                ok = wait_flag(args.flags + ((size_t)before * H + h) * args.roles + ri, D1 / 16, &s_wait);
+                if (!ok && lane == 0) atomicOr(flag, kLinFailed);
+            }
             const float* own = chained ? role.seg + ((size_t)before * H + h) * zsize
                              : scanned ? role.seg + ((size_t)sidx * H + h) * zsize : nullptr;
             const float* given = role.s_in ? role.s_in + user : nullptr;
@@ -694,12 +703,15 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                 if (hand || role.transposed) write_columns<D1>(to, row, j0, v);
                 else write_rows<D2>(to, stage, 32 * quad, j0, lane, v);
             }
-            if (hand) raise_flag(args.flags + ((size_t)sidx * H + h) * args.roles + ri);
+            if (hand) raise_flag(flag);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && s_wait.abort && args.hdr) flag_error(args.hdr, kStatusTimeout);
+    if (tid == 0 && s_wait.abort) {
+        if (args.hdr) flag_error(args.hdr, kStatusTimeout);
+        if (flag) atomicOr(flag, kLinFailed);
+    }
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

@@ -497,7 +497,8 @@ kda_status kda_debug_drop_copy(long long wait_cycles);
  * The same for the next kda_linear_chunk_fwd with bf16 inputs on this host thread
  * (one call only): its chunk kernel's first block leaves out the query tile of its
  * third chunk (of its last one, if it has fewer) and every wait of the call is
- * capped at `wait_cycles` cycles.  0 disarms.
+ * capped at `wait_cycles` cycles; where segments follow one another, each sequence's
+ * first segment does, for every head.  0 disarms.
  */
 kda_status kda_linear_debug_drop_copy(long long wait_cycles);
 

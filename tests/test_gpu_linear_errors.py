@@ -70,3 +70,28 @@ def test_a_failed_call_does_not_fail_the_next(cuda_device, failing, after):
             assert kda.lib().kda_workspace_status(ws.data_ptr(), ws.nbytes, capturing) != 0
     got = call()
     assert len(got) == len(expected) and all(torch.equal(a, b) for a, b in zip(got, expected))
+
+
+def test_a_chain_of_segments_gives_up_once(cuda_device):
+    """Segments that follow one another: the ones behind a wait that has run out do not wait for themselves."""
+    cap = 40_000_000      # cycles, some 20 ms
+    took = {}
+    for name, (B, T, H, segments) in dict(one=(1, 100, 2, 1), chain=(5, 16384, 32, 8)).items():
+        x, out, l = _layer(B=B, T=T, H=H, d=64)
+        ws = torch.empty(kda.linear_chunk_fwd_workspace_size(B, T, H, 64, 64, B, False, torch.bfloat16), dtype=torch.uint8,
+                         device="cuda")
+        assert segments == 1 or ws.nbytes >= segments * B * H * 64 * 64 * 4
+        kda.linear_chunk_fwd(**x, log_decay=l, **out, workspace=ws)
+        good = out["o"].clone()
+        assert kda.workspace_status(ws) == 0
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        kda.linear_debug_drop_copy(cap)
+        start.record()
+        kda.linear_chunk_fwd(**x, log_decay=l, **out, workspace=ws)
+        end.record()
+        assert kda.workspace_status(ws) == 4      # KDA_ERR_TIMEOUT
+        took[name] = start.elapsed_time(end)
+        kda.linear_chunk_fwd(**x, log_decay=l, **out, workspace=ws, check=True)
+        assert torch.equal(out["o"], good)
+    # 160 first segments on 148 SMs run out of time in two turns; 8 x 160 segments would in nine
+    assert took["one"] > 10 and took["chain"] < 3.5 * took["one"], took
