@@ -128,8 +128,7 @@ struct LinArgs {
     bool bf16;
     LinMap map;
     int max_segments;             // host bound on map.segments()
-    bool split;                   // some sequence may have more than one segment
-    bool scanned;                 // and the scan has turned sums into entering states
+    bool scanned;                 // sequences are cut, and the scan has turned sums into entering states
     bool chained;                 // segments take their entering state from the one before
     int* flags;                   // chained: [segments][H][roles] warps that have left their part of the state; a bit where it will not come
     int roles, slices;            // slices: column slices of the CUDA-core kernel, of the widest role

@@ -163,7 +163,6 @@ LinArgs common_args(const Plan& p, const float* log_decay, const int32_t* cu, in
     a.map.tab = cu ? reinterpret_cast<int32_t*>(ws + p.tab_off) : nullptr;
     a.map.N = p.N; a.map.T = T; a.map.seg_tok = p.seg_tok; a.map.num_seg = p.num_seg; a.map.pieces = 1;
     a.max_segments = p.max_segments;
-    a.split = p.split;
     a.hdr = static_cast<WsHeader*>(workspace);
     a.stream = static_cast<cudaStream_t>(stream);
     return a;

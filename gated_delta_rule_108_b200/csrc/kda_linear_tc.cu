@@ -96,10 +96,9 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
 
 // Zeroes rows L..127 of a tile (another sequence's tokens): they are contracted
 // over with weights of zero, which must not meet an infinity or a NaN.
-__device__ __forceinline__ void clear_rows(unsigned char* tile, int D, int L, int lo, int hi, int t, int nthreads) {
-    const int first = max(L, lo), n = max(hi - first, 0);
-    for (int e = t; e < n * (D / 8); e += nthreads) {
-        const int r = first + e / (D / 8), c = e % (D / 8);
+__device__ __forceinline__ void clear_rows(unsigned char* tile, int D, int L, int t, int nthreads) {
+    for (int e = t; e < (C - L) * (D / 8); e += nthreads) {
+        const int r = L + e / (D / 8), c = e % (D / 8);
         *reinterpret_cast<uint4*>(tile + (c >> 3) * kTile + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
 }
@@ -613,8 +612,8 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
             ok = lin_wait_warp(&full_b[n & 1], (n >> 1) & 1, &s_wait) && lin_wait_warp(&full_c[n & 1], (n >> 1) & 1, &s_wait);
             if (!ok) break;
             if (L < C) {        // P's MMA may still read b: its columns past L are dropped when P is weighted
-                clear_rows(buf_b(n), D1, L, 0, C, t, 256);
-                clear_rows(buf_c(n), D2, L, 0, C, t, 256);
+                clear_rows(buf_b(n), D1, L, t, 256);
+                clear_rows(buf_c(n), D2, L, t, 256);
                 fence_proxy_async_smem();
             }
 #pragma unroll 1
@@ -878,7 +877,7 @@ __device__ __forceinline__ void linear_sum_tc_body(const LinTcParams& prm, int r
             ok = lin_wait_warp(&full[n & 1], (n >> 1) & 1, &s_wait);
             if (!ok) break;
             if (L < C) {
-                clear_rows(bt, D1, L, 0, C, tid, 512);
+                clear_rows(bt, D1, L, tid, 512);
                 fence_proxy_async_smem();
             }
 #pragma unroll 1

@@ -102,7 +102,7 @@ qk_norm_rope_kernel(const __grid_constant__ NormArgs a)
     const int half = a.rot / 2;
     // first channels of the lane's two groups
     const bool paired = !INTER && 4 * l < half;    // (j, j + half)
-    const int e0 = INTER ? 8 * l : paired ? 4 * l : a.rot + 8 * l - 2 * half;
+    const int e0 = paired ? 4 * l : 8 * l;
     const int e1 = paired ? e0 + half : e0 + 4;
     const bool turns = mine && (INTER ? e0 < a.rot : paired);
 

@@ -123,11 +123,12 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// ------------------------------------------------------------------ TMA ---
 // Barrier `id` among `threads` threads, whole warps.
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+
+// ------------------------------------------------------------------ TMA ---
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
