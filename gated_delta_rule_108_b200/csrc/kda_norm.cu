@@ -316,6 +316,8 @@ Extent strided(const void* p, const int64_t* s, int B, int T, int H, int d, int 
 bool is_dense(const int64_t* s, int B, int T, int H, int d) {
     return (H == 1 || s[2] == d) && (T == 1 || s[1] == (int64_t)H * d) && (B == 1 || s[0] == (int64_t)T * H * d);
 }
+// A step of s elements, n - 1 times, stays below `reach` (without a product that could wrap).
+bool within(int64_t s, int64_t n, int64_t reach) { return s > -reach && s < reach && (n < 2 || std::abs(s) <= (reach - 1) / n); }
 bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 size_t partial_bytes(int d) { return sizeof(float) * 2 * (size_t)d * kMaxCtas; }
@@ -353,8 +355,13 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
             if (qs[i] % per16 || ks[i] % per16)
                 return (kda_status)set_error(KDA_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
         const int64_t reach = (int64_t)1 << 31;   // of a token's heads, whose offsets are 32 bits
-        if (std::abs(qs[2]) * Hq >= reach || std::abs(ks[2]) * Hk >= reach || (int64_t)std::max(Hq, Hk) * d >= reach)
+        if (!within(qs[2], Hq, reach) || !within(ks[2], Hk, reach) || (int64_t)std::max(Hq, Hk) * d >= reach)
             return (kda_status)set_error(KDA_ERR_UNSUPPORTED, "the heads of one token span 2^31 elements or more");
+        const int64_t memory = (int64_t)1 << 46;  // elements; no GPU's addresses reach further
+        const int64_t n[2] = {B, T};
+        for (int i = 0; i < 2; ++i)
+            if (n[i] > 1 && (!within(qs[i], n[i], memory) || !within(ks[i], n[i], memory)))
+                return (kda_status)set_error(KDA_ERR_UNSUPPORTED, "queries or keys span 2^46 elements or more");
         // an output may be its own input, contiguous: each row is read before it is written
         const int es = dtype == KDA_BF16 ? 2 : 4;
         const Extent xq = strided(q, qs, B, T, Hq, d, es), xk = strided(k, ks, B, T, Hk, d, es);
