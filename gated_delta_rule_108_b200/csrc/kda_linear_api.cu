@@ -135,7 +135,7 @@ kda_status check_workspace(void* workspace, size_t bytes, size_t need) {
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const char *x = (const char*)a, *y = (const char*)b;
-    return a && b && x < y + nb && y < x + na;
+    return a && b && na && nb && x < y + nb && y < x + na;
 }
 
 struct Span { const void* p; size_t bytes; };
@@ -234,12 +234,14 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
     if (!aligned16(initial_state)) return fail(KDA_ERR_INVALID_ARG, "initial_state misaligned");
     if (!aligned16(final_state)) return fail(KDA_ERR_INVALID_ARG, "final_state misaligned");
     const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
-    // a state may be updated in place, but not be moved by less than its size
-    const Span out[] = {{o, vbytes}, {final_state, state_bytes}};
-    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {initial_state != final_state ? initial_state : nullptr, state_bytes}};
-    if (any_overlap(out, 2, in, 4)) return fail(KDA_ERR_INVALID_ARG, "an output overlaps an input or the other output");
     st = check_workspace(workspace, workspace_bytes, p.total);
     if (st != KDA_OK) return st;
+    // a state may be updated in place, but not be moved by less than its size
+    const Span out[] = {{o, vbytes}, {final_state, state_bytes}, {workspace, p.total}};
+    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {initial_state != final_state ? initial_state : nullptr, state_bytes},
+                       {log_decay, sizeof(float) * (size_t)H}, {cu_seqlens, sizeof(int32_t) * ((size_t)p.N + 1)}};
+    if (any_overlap(out, 3, in, 6))
+        return fail(KDA_ERR_INVALID_ARG, "an output or the workspace overlaps an input, another output or the workspace");
 
     LinArgs a = common_args(p, log_decay, cu_seqlens, B, T, H, dk, dv, dtype, workspace, stream);
     const void* x[4] = {q, k, v, nullptr};
@@ -282,11 +284,13 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, con
     if (!aligned16(d_final_state)) return fail(KDA_ERR_INVALID_ARG, "d_final_state misaligned");
     if (!aligned16(d_initial_state)) return fail(KDA_ERR_INVALID_ARG, "d_initial_state misaligned");
     const size_t state_bytes = (size_t)p.N * H * dk * dv * sizeof(float);
-    const Span out[] = {{dq, kbytes}, {dk_out, kbytes}, {dv_out, vbytes}, {d_initial_state, state_bytes}};
-    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {d_o, vbytes}, {initial_state, state_bytes}, {d_final_state, state_bytes}};
-    if (any_overlap(out, 4, in, 6)) return fail(KDA_ERR_INVALID_ARG, "a gradient overlaps an input or another gradient");
     st = check_workspace(workspace, workspace_bytes, p.total);
     if (st != KDA_OK) return st;
+    const Span out[] = {{dq, kbytes}, {dk_out, kbytes}, {dv_out, vbytes}, {d_initial_state, state_bytes}, {workspace, p.total}};
+    const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {d_o, vbytes}, {initial_state, state_bytes}, {d_final_state, state_bytes},
+                       {log_decay, sizeof(float) * (size_t)H}, {cu_seqlens, sizeof(int32_t) * ((size_t)p.N + 1)}};
+    if (any_overlap(out, 5, in, 8))
+        return fail(KDA_ERR_INVALID_ARG, "a gradient or the workspace overlaps an input, another gradient or the workspace");
 
     LinArgs a = common_args(p, log_decay, cu_seqlens, B, T, H, dk, dv, dtype, workspace, stream);
     const void* x[4] = {q, k, v, d_o};
@@ -317,8 +321,8 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
             return fail(KDA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
         const size_t es = dtype == KDA_BF16 ? 2 : 4, kbytes = (size_t)B * H * dk * es, vbytes = (size_t)B * H * dv * es;
         const Span out[] = {{o, vbytes}, {state_inout, (size_t)B * H * dk * dv * sizeof(float)}};
-        const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}};
-        if (any_overlap(out, 2, in, 3)) return fail(KDA_ERR_INVALID_ARG, "o or the state overlaps another tensor");
+        const Span in[] = {{q, kbytes}, {k, kbytes}, {v, vbytes}, {log_decay, sizeof(float) * (size_t)H}};
+        if (any_overlap(out, 2, in, 4)) return fail(KDA_ERR_INVALID_ARG, "o or the state overlaps another tensor");
     }
     LinStepArgs a{};
     a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.state = state_inout; a.o = o;

@@ -318,7 +318,7 @@ bool is_dense(const int64_t* s, int B, int T, int H, int d) {
 }
 // A step of s elements, n - 1 times, stays below `reach` (without a product that could wrap).
 bool within(int64_t s, int64_t n, int64_t reach) { return s > -reach && s < reach && (n < 2 || std::abs(s) <= (reach - 1) / n); }
-bool meet(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
+bool meet(const Extent& a, const Extent& b) { return a.lo && b.lo && a.lo < b.hi && b.lo < a.hi; }
 
 size_t partial_bytes(int d) { return sizeof(float) * 2 * (size_t)d * kMaxCtas; }
 
@@ -345,6 +345,10 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
     if (st != KDA_OK) return st;
     const int64_t tokens = (int64_t)B * T;
     const bool sums = bwd && (dwq || dwk);
+    const int64_t wbytes = (int64_t)sizeof(float) * d;
+    const Extent shared_in[4] = {dense(wq, wbytes), dense(wk, wbytes), dense(inv_freq, (int64_t)sizeof(float) * (rot / 2)),
+                                 dense(positions, (int64_t)sizeof(int32_t) * tokens)};
+    Extent rows[6] = {};               // inputs, outputs, cotangents
     if (tokens > 0) {
         if (!q || !k || !oq || !ok_ || (bwd && (!dyq || !dyk)) || (rot && !inv_freq))
             return (kda_status)set_error(KDA_ERR_INVALID_ARG, "null pointer");
@@ -373,13 +377,26 @@ kda_status run_norm(const void* q, const void* k, const void* dyq, const void* d
             const Extent gq = dense(dyq, tokens * Hq * d * es), gk = dense(dyk, tokens * Hk * d * es);
             if (meet(yq, gq) || meet(yq, gk) || meet(yk, gq) || meet(yk, gk))
                 return (kda_status)set_error(KDA_ERR_INVALID_ARG, "an output overlaps a cotangent");
+            rows[4] = gq;
+            rows[5] = gk;
         }
+        for (const Extent& x : shared_in)
+            if (meet(yq, x) || meet(yk, x))
+                return (kda_status)set_error(KDA_ERR_INVALID_ARG, "an output overlaps a weight, the frequencies or the positions");
+        rows[0] = xq; rows[1] = xk; rows[2] = yq; rows[3] = yk;
     }
     if (sums) {
         if (!workspace || workspace_bytes < partial_bytes(d))
             return (kda_status)set_error(KDA_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, partial_bytes(d));
         if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
             return (kda_status)set_error(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        const Extent out[3] = {dense(dwq, wbytes), dense(dwk, wbytes), dense(workspace, (int64_t)partial_bytes(d))};
+        bool bad = meet(out[0], out[1]) || meet(out[0], out[2]) || meet(out[1], out[2]);
+        for (const Extent& y : out) {
+            for (const Extent& x : shared_in) bad |= meet(y, x);
+            for (const Extent& x : rows) bad |= meet(y, x);
+        }
+        if (bad) return (kda_status)set_error(KDA_ERR_INVALID_ARG, "a weight gradient or the workspace overlaps another tensor");
     }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

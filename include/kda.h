@@ -341,9 +341,9 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
  *  log_decay   [H]             fp32, <= 0; -inf forgets everything at each token;
  *              NULL: no decay (lambda = 1)
  *  initial_state, cu_seqlens, final_state, o, sizes: as kda_chunk_fwd (sequences
- *              may be empty: their final state is their initial state); the
- *              outputs must not overlap each other or an input, but final_state
- *              may be initial_state
+ *              may be empty: their final state is their initial state); outputs
+ *              and workspace must not overlap each other or an input, but
+ *              final_state may be initial_state
  *  workspace   at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte
  *              aligned; its contents on entry do not matter.  Where the size is 256,
  *              the status alone, NULL is allowed: then the call has no status.
@@ -386,7 +386,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v,
  *
  * (G_T also holds d_final_state).  Arguments as kda_linear_chunk_fwd and
  * kda_chunk_bwd; d_final_state NULL: zeros; d_initial_state NULL: not computed.
- * Outputs must not overlap inputs or each other.
+ * Outputs and workspace must not overlap inputs or each other.
  */
 size_t kda_linear_chunk_bwd_workspace_size(int B, int T, int H, int dk, int dv,
                                            int num_seqs, int varlen, kda_dtype dtype);
@@ -431,7 +431,8 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
  *  d           a multiple of 8 up to 256; rotary_dim a multiple of 16 up to d
  *  eps         > 0: a row of zeros gives zeros
  *  q_out       [B, T, Hq, d], k_out [B, T, Hk, d] dtype, contiguous, written; each
- *              may be its (contiguous) input itself, and must not overlap it otherwise
+ *              may be its (contiguous) input itself, and must not overlap it otherwise,
+ *              nor any other of the tensors
  */
 typedef enum { KDA_NORM_RMS = 0, KDA_NORM_L2 = 1 } kda_norm;
 kda_status kda_qk_norm_rope(const void* q, const void* k, const float* q_weight,
@@ -448,7 +449,7 @@ kda_status kda_qk_norm_rope(const void* q, const void* k, const float* q_weight,
  * if not wanted).  The sums over tokens run in a fixed order.  With either weight
  * gradient the workspace needs kda_qk_norm_rope_bwd_workspace_size(d) bytes,
  * 256-byte aligned; otherwise it may be NULL.  Other arguments as kda_qk_norm_rope
- * (q, k: its inputs).  dq and dk must not overlap the inputs.
+ * (q, k: its inputs).  Outputs and workspace must not overlap inputs or each other.
  */
 size_t kda_qk_norm_rope_bwd_workspace_size(int d);
 kda_status kda_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out,
