@@ -6,6 +6,8 @@ import torch
 
 import linear_plain as P
 from gated_delta_rule_108_b200 import kda
+from linear_precision import assert_near
+from test_gpu_linear import DTYPES, case, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +85,37 @@ def test_no_output_depends_on_another_being_asked_for(cuda_device, B, T, H, lens
     full = kda.linear_chunk_bwd(q, k, v, l, d_o, cu_seqlens=cu)
     r = kda.linear_chunk_bwd(q, k, v, l, d_o, cu_seqlens=cu, output_d_initial_state=False)
     assert r["dS0"] is None and all(torch.equal(r[n], full[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("decay", ["slopes", "strong", "none"])
+@pytest.mark.parametrize("T,dk,dv,lens", [(63, 128, 128, None), (128, 64, 128, None), (300, 128, 64, None), (413, 128, 128, None),
+                                          (1500, 64, 64, None), (700, 64, 128, (1, 420, 0, 279))], ids=str)
+def test_results_in_norm(cuda_device, T, dk, dv, lens, decay, dtype):
+    x, back = case(1, T, 2, dk, dv, dtype, decay=decay, lens=lens, seed=40 + T)
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    ref, Sf, _, _ = P.forward(x["q"], x["k"], x["v"], x["log_decay"], x["initial_state"], x["cu_seqlens"])
+    assert_near(o, ref, "o", dtype)
+    assert_near(S, Sf, "final_state")
+    r = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
+    g, _ = P.backward(x["q"], x["k"], x["v"], x["log_decay"], back["d_o"], x["initial_state"], back["d_final_state"],
+                      x["cu_seqlens"])
+    for n in ("dq", "dk", "dv"):
+        assert_near(r[n], g[n], n, dtype)
+    assert_near(r["dS0"], g["dS0"], "dS0")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("H,d", [(1, 128), (140, 64)])
+def test_states_of_long_sequences(cuda_device, H, d, dtype):
+    """16,384 tokens without a decay, one head (cut into segments) and as many as SMs (128 chunks
+    in a row): the states are plain sums of products."""
+    T = 16384
+    g = torch.Generator(device="cuda").manual_seed(50)
+    q, k, v, d_o = (torch.randn(1, T, H, d, generator=g, device="cuda").to(dtype) for _ in range(4))
+    _, S = kda.linear_chunk_fwd(q, k, v, None, check=True)
+    r = kda.linear_chunk_bwd(q, k, v, None, d_o, check=True)
+    for h in sorted({0, H // 2, H - 1}):
+        heads = [t[0, :, h].double() for t in (q, k, v, d_o)]
+        assert_near(S[0, h], heads[1].T @ heads[2], "final_state")
+        assert_near(r["dS0"][0, h], d ** -0.5 * heads[0].T @ heads[3], "dS0")
