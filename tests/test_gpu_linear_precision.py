@@ -7,7 +7,7 @@ import torch
 import linear_plain as P
 from gated_delta_rule_108_b200 import kda
 from linear_precision import assert_near
-from test_gpu_linear import DTYPES, case, ids
+from test_gpu_linear import DTYPES, case, check_bwd, check_fwd, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,31 @@ def test_states_of_long_sequences(cuda_device, H, d, dtype):
         heads = [t[0, :, h].double() for t in (q, k, v, d_o)]
         assert_near(S[0, h], heads[1].T @ heads[2], "final_state")
         assert_near(r["dS0"][0, h], d ** -0.5 * heads[0].T @ heads[3], "dS0")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("decay", ["slopes", "strong", "none"])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("lens", [None, (3000, 0, 1, 99)], ids=str)
+def test_scanned_segments(cuda_device, lens, dk, dv, decay, dtype):
+    """More than eight segments a sequence, forward and backward: several heads, unequal head sizes, initial states."""
+    T, H, N = 3100, 2, 1 if lens is None else len(lens)
+    for size, roles in ((kda.linear_chunk_fwd_workspace_size, 1), (kda.linear_chunk_bwd_workspace_size, 3)):
+        slots = (size(1, T, H, dk, dv, N, lens is not None, dtype) - 256) // (H * dk * dv * 4 * roles)
+        assert slots - (0 if lens is None else N) >= (9 if lens is None else 8)      # packed: one more than that per sequence
+    x, back = case(1, T, H, dk, dv, dtype, decay=decay, lens=lens, seed=60)
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    check_fwd(x, o, S)
+    assert_near(S, P.forward(x["q"], x["k"], x["v"], x["log_decay"], x["initial_state"], x["cu_seqlens"])[1], "final_state")
+    r = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
+    check_bwd(x, back, r)
+
+
+@pytest.mark.parametrize("lens", [None, (1500, 1600)], ids=str)
+def test_scanned_segments_of_many_heads(cuda_device, lens):
+    """Seven heads that decay at seven rates."""
+    x, back = case(1, 3100, 7, 64, 128, torch.bfloat16, decay="strong", lens=lens, seed=61)
+    x["log_decay"][-1] = -0.3
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    check_fwd(x, o, S)
+    check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
