@@ -29,9 +29,9 @@ namespace kda {
 constexpr int kLinChunk = 128;    // tokens per chunk: the rows of one tensor-core tile
 constexpr int kLinMaxRoles = 3;
 // Segments per sequence up to which no scan is launched: each CTA adds up the sums before
-// it itself.  Without and with the scan: two segments (B=4, T=4096, H=16) 105 and 116 us,
-// four (T=4096, H=32) 62 and 67 us, eight (T=8192, H=16) 65 and 64 us, eleven (B=2,
-// T=8192, H=20) 157 and 156 us, sixteen (T=4096, H=8) 37.5 and 31.5 us.
+// it itself.  Without and with the scan: two segments (B=4, T=4096, H=16) 121 and 130 us,
+// four (T=4096, H=32) 75 and 78 us, eight (T=8192, H=16) 79 and 75 us, eleven (B=2,
+// T=8192, H=20) 195 and 181 us, sixteen (T=4096, H=8) 48.5 and 33.1 us.
 constexpr int kLinDirect = 8;
 
 struct LinRole {
@@ -196,8 +196,8 @@ __device__ __forceinline__ int lin_skip(double l, int len, int chunk, int chunks
 // call asks), and again if this launch itself is refused, as after a reset of the
 // device; an error that an earlier call has left says nothing about this one.  With
 // `follows` the blocks may start while the kernel before, of the same call, ends; they
-// wait for it in lin_begin.  T=2048, H=8: 25.7 us without, 24.6 with; five packed
-// sequences 25.2 and 24.2.
+// wait for it in lin_begin.  T=2048, H=8: 26.8 us without, 26.0 with; five packed
+// sequences 30.8 and 30.0.
 inline cudaError_t lin_launch(const void* kernel, size_t grid, int threads, int smem_bytes, void** args,
                               bool follows, cudaStream_t stream, std::atomic<uint64_t>& done) {
     int dev = 0;

@@ -26,10 +26,15 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // How long the segments of a sequence of `chunks` chunks are, when `chains` CTAs work
 // on each segment number, and in how many pieces each is summed: the cheapest by the
-// count of waves over the SMs.  In units of one chunk of the chunk kernel (3.8 us at
+// count of waves over the SMs.  In units of one chunk of the chunk kernel (8,050 cycles at
 // dk = dv = 128), as measured: a chunk of the summing pass 0.5, a CTA 1.5 to start and
 // end (1 there), its launch 2.  Pieces only where no scan follows.  B=4, T=4096, H=16 (64
-// chains of 32 chunks, two segments): 106 us in one piece, 98 in two.
+// chains of 32 chunks, two segments): 120 us in one piece, 109 in two.  The same units
+// serve fp32 and d = 64: of 28 forwards and gradients of either type (1,021 to 32,768
+// tokens, 4 to 64 heads and sequences, d 64 and 128), each with 1 to 32 segments, 24 came
+// within 3 % of the best with the plan's choice, uncut or not (fp32, T=4096, H=8: 969 us
+// uncut, 178 in the plan's eight; B=4, T=4096, H=16: 973 uncut as planned, 1,156 in two),
+// and the worst at 1.18 times (fp32, d = 64, B=2, T=8192, H=20: 519 us in three, 438 in twelve).
 int plan_segment_chunks(int64_t chains, int64_t chunks, double& best, int& pieces) {
     int64_t best_len = std::max<int64_t>(chunks, 1);
     best = 0;
@@ -52,8 +57,8 @@ int plan_segment_chunks(int64_t chains, int64_t chunks, double& best, int& piece
 
 // The same where segments follow one another: n of them take n turns at least; 2.5 for
 // a segment's start and end with the state handed on, 1 for clearing the flags.  The
-// gradients at B=4, T=4096, H=16 (192 chains of 32 chunks): 248 us uncut, 210 in two,
-// 209 in three, 253 in four segments.
+// gradients at B=4, T=4096, H=16 (192 chains of 32 chunks): 283 us uncut, 229 in two,
+// 222 in three, 250 in four segments.
 int plan_chained_chunks(int64_t chains, int64_t chunks, double& best) {
     int64_t best_len = 0;
     for (int64_t s = 2; s <= std::min<int64_t>(chunks, 16); ++s) {
@@ -97,7 +102,7 @@ bool make_plan(int B, int T, int H, int dk, int dv, int num_seqs, bool varlen, k
     if (!p.split || p.num_seg * p.pieces > kLinDirect) p.pieces = 1;
     // packed: every sequence may end in a short segment; unsplit when the longest is
     // within 1.75 times one SM's share.  H=16, cut and not: longest at 1.2 shares (of
-    // 65,536 tokens in 15 sequences) 380 and 257 us, at 1.6 389 and 356, at 3 406 and 575
+    // 65,536 tokens in 15 sequences) 437 and 320 us, at 1.6 428 and 408, at 3 488 and 732
     const int64_t most = varlen ? (int64_t)p.N + T / p.seg_tok : (int64_t)p.N * p.num_seg;
     if (most * p.pieces * H * per_head >= (int64_t)1 << 31) return false;
     p.max_segments = (int)most;

@@ -106,8 +106,8 @@ linear_prep_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, 
     }
 }
 
-// The same for at most 32 sequences by one warp, a lane each: a forward of 5 sequences takes 25.2
-// us with it and 27.1 with the kernel above, of 32 43.8 and 45.7.
+// The same for at most 32 sequences by one warp, a lane each: a forward of 5 sequences takes 29.8
+// us with it and 31.8 with the kernel above, of 32 40.6 and 42.5.
 __global__ void __launch_bounds__(32)
 linear_prep_few_kernel(WsHeader* hdr, int32_t* tab, const int32_t* __restrict__ cu, int N, int T, int seg_tok,
                        int balance_tokens)

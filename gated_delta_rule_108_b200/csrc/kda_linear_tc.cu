@@ -18,11 +18,11 @@
 //    fp32 in TMEM.  y's own rounding is no measure for it: a row of a may read Z from
 //    a direction in which Z holds little, and what a part leaves out scales with
 //    |Z| |a|, not with y (one part, and keys within 0.1 of a direction that the queries
-//    are orthogonal to: o off by ten times its rounding).  The second part costs 6 to
-//    12 % of a forward;
+//    are orthogonal to: o off by ten times its rounding).  The second part costs 8 to
+//    14 % of a forward;
 //  - the weighted c in three parts (2^-24) in the roles whose state is a result (of the
 //    forward, of dv), in two where it only reaches y: a state is a sum over the whole sequence, and fp32 is what
-//    it is returned in (two parts everywhere would save 0.4 us of 4.5 us a chunk).
+//    it is returned in (two parts everywhere would save 6 %: B=9, T=4096, H=16 153 instead of 163 us).
 // The tensor core cuts its sums off instead of rounding them, always towards zero.
 // So each chunk's sum U starts from zero and is added to Z in registers, rounded:
 // after 16,384 tokens without decay the state is off by 1.8e-7 of its size, 5.7e-6
@@ -35,13 +35,13 @@
 // operands -> Z^T a, U) and the rest overlap: b and c have two buffers each, so the next
 // chunk's tiles are in flight while this one is worked on; a's buffer frees as soon as
 // P and Z^T a are done; y leaves through the buffer of its own chunk's c (warp 18 sends
-// it out by TMA; stored straight from registers a chunk takes 5.2 us instead of 4.6).
+// it out by TMA; stored straight from registers a chunk took 5.2 us instead of 4.6).
 //
-// What bounds it is shared memory: a chunk's MMAs read 384 KB of operands (3,072
-// cycles), TMA moves 128 KB (1,024) and the warps 2,900 wavefronts, 7,000 cycles
-// together, and a chunk takes 6,900.  B=9, T=4096, H=16 (144 CTAs of 32 chunks): 145 us,
-// tensor pipe 52 %, issue 46 %, DRAM 4.1 TB/s; 3.8 us a chunk at the full clock, 4.5 at
-// the clock that the power limit leaves in long runs.
+// What bounds it is shared memory: a chunk's MMAs read 448 KB of operands (3,584
+// cycles), TMA moves 128 KB (1,024) and the warps 3,260 wavefronts, 7,870 cycles
+// together, and a chunk takes 8,050.  B=9, T=4096, H=16 (144 CTAs of 32 chunks): 151 us
+// under the counters (tensor pipe 49 %, issue 46 %, DRAM 3.9 TB/s), 165 us in short runs,
+// 191 us at the clock that the power limit leaves in long ones.
 //
 // Every wait is bounded; one that gives up sets a flag that ends the CTA's other
 // waits, records KDA_ERR_TIMEOUT, and the CTA waits for its own copies and MMAs,

@@ -12,10 +12,11 @@
 //   dx = r h - m r^3 <h, x> x,   dw = sum over tokens and heads of g r x
 //
 // Both read each row once and write it once: HBM bandwidth bounds them at size (65,536
-// tokens of 32 + 8 heads, d = 128: 227 us, 5.9 TB/s, 90 % of a plain copy's rate, issue
-// 54 %; the gradients of 4 x 4096 tokens of 16 + 16 heads 80 us, 77 %, where the weights'
-// sums hold 128 registers and leave two CTAs an SM), launch latency for a handful of
-// tokens.  A lane holds eight channels of a row, in
+// tokens of 32 + 8 heads, d = 128: 226 us in short runs, 91 % of a plain copy's rate, and
+// 242 us, 85 %, at the clock that the power limit leaves in long ones, issue 54 %; the
+// gradients of 4 x 4096 tokens of 16 + 16 heads 82 us, 75 %, and 86 us, 71 %, where the
+// weights' sums hold 128 registers and leave two CTAs an SM), launch latency for a
+// handful of tokens.  A lane holds eight channels of a row, in
 // two groups of four chosen so that the two channels of a pair lie in one lane
 // (4 l.. and 4 l + rotary_dim / 2.. where halves are paired), so LPR = d / 8 lanes
 // (rounded up to 8, 16 or 32) share a row, a warp takes 32 / LPR rows at a time and
