@@ -21,8 +21,9 @@
 //    are orthogonal to: o off by ten times its rounding).  The second part costs 8 to
 //    14 % of a forward;
 //  - the weighted c in three parts (2^-24) in the roles whose state is a result (of the
-//    forward, of dv), in two where it only reaches y: a state is a sum over the whole sequence, and fp32 is what
-//    it is returned in (two parts everywhere would save 6 %: B=9, T=4096, H=16 153 instead of 163 us).
+//    forward, of dv), in two where it only reaches y: a state is a sum over the whole
+//    sequence, and fp32 is what it is returned in (two parts everywhere would save 6 %:
+//    B=9, T=4096, H=16 153 instead of 163 us).
 // The tensor core cuts its sums off instead of rounding them, always towards zero.
 // So each chunk's sum U starts from zero and is added to Z in registers, rounded:
 // after 16,384 tokens without decay the state is off by 1.8e-7 of its size, 5.7e-6
@@ -491,10 +492,13 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                 if (rev ? b >= quad : b <= quad) {      // these rows see this block of columns
                     float v[32];
                     tmem_ld32_sync(at, v);
-                    if (L < C) {                        // columns past L hold other tokens' products
+                    // columns past L hold other tokens' products, and on the diagonal's other side one may be infinite
+                    if (L < C || b == quad) {
+                        uint32_t keep = L >= 32 * b + 32 ? ~0u : L > 32 * b ? (1u << (L - 32 * b)) - 1 : 0u;
+                        if (b == quad) keep &= rev ? ~0u << lane : ~0u >> (31 - lane);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (32 * b + j >= L) v[j] = 0.f;
+                            if (!(keep >> j & 1)) v[j] = 0.f;
                     }
                     // off the diagonal |r - i| = (distance to the block's near edge) + (distance within it): both factors <= 1
                     const bool on = b == quad;

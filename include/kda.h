@@ -364,7 +364,8 @@ kda_status kda_chunk_bwd_saved(const void* q, const void* k, const void* v,
  * rounding and by up to 2^-14 of the sum of the magnitudes it is made of, which
  * shows where that sum nearly cancels.  The states keep fp32 (the factors that
  * enter them are split into three bf16 parts).  fp32 inputs are computed in fp32 on
- * CUDA cores.
+ * CUDA cores.  Powers of lambda, and weighted products <q_t, k_i>, below 2^-126 may
+ * count as zero.
  * Inputs must be finite: an infinity or a NaN at one token reaches every output
  * of its chunk of 128 tokens, also those before it.  It does not reach other
  * sequences.

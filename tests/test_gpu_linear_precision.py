@@ -147,3 +147,37 @@ def test_scanned_segments_of_many_heads(cuda_device, lens):
     o, S = kda.linear_chunk_fwd(**dev(x), check=True)
     check_fwd(x, o, S)
     check_bwd(x, back, kda.linear_chunk_bwd(**dev(x), **dev(back), check=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("T,decay", [(100, "slopes"), (128, "none"), (300, "strong")])
+def test_products_that_no_output_holds_may_overflow(cuda_device, T, decay, dtype):
+    """A query against a later key, a cotangent against a later value: beyond fp32's range, and not part of any result."""
+    x, back = case(1, T, 2, 64, 128, dtype, decay=decay, seed=90)
+    x["initial_state"][:, :, 0], back["d_final_state"][:, :, 0] = 0, 0
+    x["q"][..., 0], x["k"][..., 0] = 0, 0
+    x["q"][:, 3, :, 0], x["k"][:, 20, :, 0] = 1e30, 1e30
+    back["d_o"][:, 5, :, 0], x["v"][:, 25, :, 0] = 1e30, 1e30
+    o, S = kda.linear_chunk_fwd(**dev(x), check=True)
+    r = kda.linear_chunk_bwd(**dev(x), **dev(back), check=True)
+    assert all(bool(t.isfinite().all()) for t in (o, S, *r.values()))
+    # As linear_plain.assert_close, and what falls below fp32's normal numbers: a weight lambda^n or
+    # an element of P below 2^-126 may be off by that much, so an output by 2^-126 of the products that
+    # its weights would leave whole (the magnitudes without a decay) and of the row of c that P meets.
+    q, k, v, d_o = (t.double().abs() for t in (x["q"], x["k"], x["v"], back["d_o"]))
+    whole = lambda c: c.sum(1, keepdim=True).expand_as(c)  # noqa: E731
+    args = x["q"], x["k"], x["v"]
+    ref, Sf, om, Sm = P.forward(*args, x["log_decay"], x["initial_state"])
+    _, _, ou, Su = P.forward(*args, None, x["initial_state"])
+    g, m = P.backward(*args, x["log_decay"], back["d_o"], x["initial_state"], back["d_final_state"])
+    _, u = P.backward(*args, None, back["d_o"], x["initial_state"], back["d_final_state"])
+    n = 2 * (300 + 24 * -(-T // 128)) * 2.0 ** -24 + 2.0 ** -22
+    for name, y, ref, mag, under, rounded in (
+            ("o", o, ref, om, ou + whole(v), True), ("final_state", S, Sf, Sm, Su, False),
+            ("dq", r["dq"], g["dq"], m["dq"], u["dq"] + whole(k), True), ("dk", r["dk"], g["dk"], m["dk"], u["dk"] + whole(q), True),
+            ("dv", r["dv"], g["dv"], m["dv"], u["dv"] + whole(d_o), True), ("dS0", r["dS0"], g["dS0"], m["dS0"], u["dS0"], False)):
+        tol = n * mag + 2.0 ** -126 * under + 1e-30
+        if rounded and dtype == torch.bfloat16:
+            tol = tol + (2.0 ** -8 + 2.0 ** -14) * ref.abs() + 3 * 2.0 ** -16 * mag
+        bad = ~((y.double().cpu() - ref).abs() <= tol)
+        assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} beyond the bound, first at {bad.nonzero()[0].tolist()}"
