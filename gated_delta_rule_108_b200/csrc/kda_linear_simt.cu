@@ -171,7 +171,7 @@ linear_scan_kernel(const __grid_constant__ LinArgs a)
     }
     // only a sequence's last segment may be short; it is the first one processed in reverse
     const int tail = first + count - 1;
-    const float w_full = lin_pow(l, a.map.locate(first).len), w_tail = lin_pow(l, a.map.locate(tail).len);
+    const float2 w_full = lin_pow2(l, a.map.locate(first).len), w_tail = lin_pow2(l, a.map.locate(tail).len);
     constexpr int AHEAD = 8;                    // sums in flight
     for (int n0 = 0; n0 < count; n0 += AHEAD) {
         float4 own[AHEAD];
@@ -187,11 +187,11 @@ linear_scan_kernel(const __grid_constant__ LinArgs a)
             const int n = n0 + k, s = role.reverse ? tail - n : first + n;
             if (n >= count) break;
             *reinterpret_cast<float4*>(role.seg + ((size_t)s * a.H + h) * size + e) = E;
-            const float w = s == tail ? w_tail : w_full;
-            E.x = fmaf(w, E.x, own[k].x);
-            E.y = fmaf(w, E.y, own[k].y);
-            E.z = fmaf(w, E.z, own[k].z);
-            E.w = fmaf(w, E.w, own[k].w);
+            const float2 w = s == tail ? w_tail : w_full;
+            E.x = decay_add(w, E.x, own[k].x);
+            E.y = decay_add(w, E.y, own[k].y);
+            E.z = decay_add(w, E.z, own[k].z);
+            E.w = decay_add(w, E.w, own[k].w);
         }
     }
 }
@@ -207,7 +207,7 @@ template <int D1>
 struct LinSimtSmem {
     struct Tile { float a[kSimtChunk * D1], b[kSimtChunk * D1], c[kSimtChunk * kSimtCols]; } tile[2];
     float p[kSimtChunk * kSimtChunk], z[D1 * kSimtCols];
-    float pw[kSimtChunk + 1];
+    float pw[kSimtChunk + 1], pw_rest[2];       // powers; second parts of those of a whole chunk and of the short one
 
     static __device__ __forceinline__ int at(int r, int group) {          // a, b
         return r * D1 + 4 * (group ^ (((r >> 2) & 3) | ((r >> 1) & 4)));
@@ -291,6 +291,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
     const float c_inter = role.c_inter, c_intra = role.c_intra, c_upd = role.c_upd;
     const double l = lin_log_decay(args.log_decay, h);
     for (int n = tid; n <= kSimtChunk; n += 256) sm.pw[n] = lin_pow(l, n);
+    if (tid >= 128 && tid < 130) sm.pw_rest[tid - 128] = lin_pow2(l, tid == 128 ? kSimtChunk : g.len % kSimtChunk).y;
 
     const size_t zsize = (size_t)D1 * D2;
     const size_t user = ((size_t)g.seq * H + h) * zsize;
@@ -343,7 +344,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
                 z[n][m][2 * q + 1] = make_float2(v.z, v.w);
             }
     if (!states_only && !scanned)
-        lin_enter(args.map, g, sidx, rev, l, [&](int slot, float w) {
+        lin_enter(args.map, g, sidx, rev, l, [&](int slot, float2 w) {
             const float* own = role.seg + ((size_t)slot * H + h) * zsize;
 #pragma unroll
             for (int n = 0; n < HALVES; ++n)
@@ -352,8 +353,8 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const float4 u = *reinterpret_cast<const float4*>(own + (size_t)row_z(n, m) * D2 + j0 + 32 * q + 4 * tx);
-                        z[n][m][2 * q] = fma2(make_float2(w, w), z[n][m][2 * q], make_float2(u.x, u.y));
-                        z[n][m][2 * q + 1] = fma2(make_float2(w, w), z[n][m][2 * q + 1], make_float2(u.z, u.w));
+                        z[n][m][2 * q] = decay_add(w, z[n][m][2 * q], make_float2(u.x, u.y));
+                        z[n][m][2 * q + 1] = decay_add(w, z[n][m][2 * q + 1], make_float2(u.z, u.w));
                     }
         });
     for (int n = 0; n < nch; ++n) {
@@ -461,7 +462,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
             __syncthreads();                     // Z has been read by all: the next chunk's goes in its place
         }
         // the chunk's sum: rows 4 ty.. and 32 + 4 ty.. of each half, tokens in groups of four
-        const float2 w = make_float2(sm.pw[L], sm.pw[L]);
+        const float2 w = make_float2(sm.pw[L], sm.pw_rest[L < kSimtChunk]);
 #pragma unroll
         for (int half = 0; half < HALVES; ++half) {
             float2 u[8][4] = {}, own[2][4];
@@ -480,7 +481,7 @@ __device__ __forceinline__ void linear_simt_body(const LinArgs& args, int ri, in
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) z[half][m][k] = fma2(w, z[half][m][k], own[m][k]);
+                for (int k = 0; k < 4; ++k) z[half][m][k] = decay_add(w, z[half][m][k], own[m][k]);
         }
     }
     float* to = states_only ? seg : (last && role.s_out ? role.s_out + user : nullptr);

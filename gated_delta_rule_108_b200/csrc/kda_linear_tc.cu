@@ -41,8 +41,8 @@
 // What bounds it is shared memory: a chunk's MMAs read 448 KB of operands (3,584
 // cycles), TMA moves 128 KB (1,024) and the warps 3,260 wavefronts, 7,870 cycles
 // together, and a chunk takes 8,050.  B=9, T=4096, H=16 (144 CTAs of 32 chunks): 151 us
-// under the counters (tensor pipe 49 %, issue 46 %, DRAM 3.9 TB/s), 165 us in short runs,
-// 191 us at the clock that the power limit leaves in long ones.
+// under the counters (tensor pipe 49 %, issue 46 %, DRAM 3.9 TB/s), 168 us in short runs,
+// 192 us at the clock that the power limit leaves in long ones.
 //
 // Every wait is bounded; one that gives up sets a flag that ends the CTA's other
 // waits, records KDA_ERR_TIMEOUT, and the CTA waits for its own copies and MMAs,
@@ -287,7 +287,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         y_done, y_free, y_staged[2], cw_ready[2], cw_free[2], upd_done, z_ready, zh_done, zl_ready, drained;
     __shared__ uint32_t s_tmem;
     __shared__ LinWait s_wait;
-    __shared__ float pw[C + 1];
+    __shared__ float pw[C + 1], pw_rest[2];     // powers; second parts of those of a whole chunk and of the short one
     // weights of a 32 x 32 block of P, at [31 + row - column] for one on the diagonal (0 on the side that does not
     // count) and [31 - column], times a factor of the row, for another
     __shared__ float diag[64], edge[32];
@@ -344,6 +344,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
     {
         const double l = lin_log_decay(args.log_decay, h);
         if (tid <= C) pw[tid] = lin_pow(l, tid);
+        else if (tid >= 256 && tid < 258) pw_rest[tid - 256] = lin_pow2(l, tid == 256 ? C : g.len % C).y;
         else if (tid >= 160 && tid < 192) edge[tid - 160] = lin_pow(l, rev ? 191 - tid : tid - 160);
         else if (tid >= 192 && tid < 255) {
             const int n = rev ? 31 - (tid - 192) : tid - 192 - 31;
@@ -601,11 +602,11 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 }
                 if (!scanned && !args.chained)
-                    lin_enter(args.map, g, sidx, rev, l, [&](int slot, float w) {
+                    lin_enter(args.map, g, sidx, rev, l, [&](int slot, float2 w) {
                         float u[32];
                         read_columns<D1>(role.seg + ((size_t)slot * H + h) * zsize, row, j0, u);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = fmaf(w, v[j], u[j]);
+                        for (int j = 0; j < 32; ++j) v[j] = decay_add(w, v[j], u[j]);
                     });
                 tmem_st32_sync(ZREG + lane_base + j0, v);
             }
@@ -636,7 +637,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                 if (!ok) break;
                 tc_fence_after();
                 if (mine) {                             // Z <- lambda^L Z + U of the previous chunk; its operand's first part
-                    const float gam = n > 0 ? pw[len_before] : 1.f;
+                    const float2 gam = n > 0 ? make_float2(pw[len_before], pw_rest[len_before < C]) : make_float2(1.f, 0.f);
 #pragma unroll 1
                     for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                         float v[32], u[32];
@@ -645,7 +646,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                             uint32_t d[32];
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
-                                const float2 x = fma2(make_float2(gam, gam), make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
+                                const float2 x = decay_add(gam, make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
                                 v[j] = x.x; v[j + 1] = x.y;
                                 d[j] = __float_as_uint(x.x);
                                 d[j + 1] = __float_as_uint(x.y);
@@ -692,7 +693,8 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
         if (ok && mine && (hand || (last && role.s_out))) {
             tc_fence_after();
             float* to = hand ? role.seg + ((size_t)sidx * H + h) * zsize : role.s_out + user;
-            const float gam = nch > 0 ? pw[min(C, g.len - chunk_of(nch - 1) * C)] : 1.f;
+            const int len = nch > 0 ? min(C, g.len - chunk_of(nch - 1) * C) : 0;
+            const float2 gam = make_float2(pw[len], len ? pw_rest[len < C] : 0.f);
 #pragma unroll 1
             for (int j0 = 32 * sub; j0 < D2; j0 += 64) {
                 float v[32];
@@ -701,7 +703,7 @@ __device__ __forceinline__ void linear_tc_body(const LinTcParams& prm, int ri, i
                     float u[32];
                     tmem_ld32_sync(UACC + lane_base + j0, u);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = fmaf(gam, v[j], u[j]);
+                    for (int j = 0; j < 32; ++j) v[j] = decay_add(gam, v[j], u[j]);
                 }
                 if (hand || role.transposed) write_columns<D1>(to, row, j0, v);
                 else write_rows<D2>(to, stage, 32 * quad, j0, lane, v);

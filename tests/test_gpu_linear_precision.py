@@ -181,3 +181,29 @@ def test_products_that_no_output_holds_may_overflow(cuda_device, T, decay, dtype
             tol = tol + (2.0 ** -8 + 2.0 ** -14) * ref.abs() + 3 * 2.0 ** -16 * mag
         bad = ~((y.double().cpu() - ref).abs() <= tol)
         assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} beyond the bound, first at {bad.nonzero()[0].tolist()}"
+
+
+def unlucky(n, lo=1e-6, hi=3e-6):
+    """A slow decay whose power e^(l n) lies as far as it can between two fp32 numbers."""
+    l = -torch.linspace(lo, hi, 20001, dtype=torch.float64).float()
+    e = (l.double() * n).exp()
+    return float(l[((e.float().double() - e) / e).abs().argmax()])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("T,H", [(65536, 4), (16384, 140)])
+def test_slow_decays_over_long_sequences(cuda_device, T, H, dtype):
+    """What a chunk leaves of a state is a power below one, taken hundreds of times: its rounding must not add up."""
+    d, N = 64, torch.arange(T, device="cuda", dtype=torch.float64)
+    g = torch.Generator(device="cuda").manual_seed(95)
+    q, k, v, d_o = (torch.randn(1, T, H, d, generator=g, device="cuda").to(dtype) for _ in range(4))
+    S0, dS = (T ** 0.5 * torch.randn(1, H, d, d, generator=g, device="cuda") for _ in range(2))
+    slow = [unlucky(64), unlucky(128), unlucky(768), unlucky(1024)]
+    l = torch.tensor([slow[h % 4] for h in range(H)], device="cuda")
+    _, S = kda.linear_chunk_fwd(q, k, v, l, S0, check=True)
+    r = kda.linear_chunk_bwd(q, k, v, l, d_o, S0, dS, check=True)
+    for h in range(4):
+        qh, kh, vh, oh = (t[0, :, h].double() for t in (q, k, v, d_o))
+        power = lambda n: (l[h].double() * n).exp()  # noqa: E731
+        assert_near(S[0, h], power(T) * S0[0, h].double() + (power(T - 1 - N)[:, None] * kh).T @ vh, f"final_state {h}")
+        assert_near(r["dS0"][0, h], power(T) * dS[0, h].double() + d ** -0.5 * (power(N + 1)[:, None] * qh).T @ oh, f"dS0 {h}")
