@@ -47,7 +47,11 @@ linear_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     float vj[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) vj[c] = to_f32(v[(size_t)bh * DV + j0 + 4 * col + c]);
-    const float a = log_decay ? expf(log_decay[bh % H]) : 1.f;
+    // lambda = m + keep with m = lambda - 1 where that is small: rounded to fp32 itself, a slow
+    // decay is off by the same 2^-25 in every token (10,000 tokens at -1e-6: 3e-4 of the state)
+    const float l = log_decay ? log_decay[bh % H] : 0.f;
+    const bool slow = l > -0.5f;
+    const float m = slow ? expm1f(l) : expf(l), keep = slow ? 1.f : 0.f;
     __syncthreads();
 
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -55,10 +59,10 @@ linear_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     for (int r = 0; r < ROWS; ++r) {
         const int i = row + r * STEP;
         const float ki = sk[i], qi = sq[i];
-        s[r].x = fmaf(ki, vj[0], a * s[r].x);
-        s[r].y = fmaf(ki, vj[1], a * s[r].y);
-        s[r].z = fmaf(ki, vj[2], a * s[r].z);
-        s[r].w = fmaf(ki, vj[3], a * s[r].w);
+        s[r].x = fmaf(ki, vj[0], fmaf(m, s[r].x, keep * s[r].x));
+        s[r].y = fmaf(ki, vj[1], fmaf(m, s[r].y, keep * s[r].y));
+        s[r].z = fmaf(ki, vj[2], fmaf(m, s[r].z, keep * s[r].z));
+        s[r].w = fmaf(ki, vj[3], fmaf(m, s[r].w, keep * s[r].w));
         __stcs(reinterpret_cast<float4*>(S + (size_t)i * DV), s[r]);
         acc.x = fmaf(qi, s[r].x, acc.x);
         acc.y = fmaf(qi, s[r].y, acc.y);

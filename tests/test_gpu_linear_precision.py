@@ -207,3 +207,42 @@ def test_slow_decays_over_long_sequences(cuda_device, T, H, dtype):
         power = lambda n: (l[h].double() * n).exp()  # noqa: E731
         assert_near(S[0, h], power(T) * S0[0, h].double() + (power(T - 1 - N)[:, None] * kh).T @ vh, f"final_state {h}")
         assert_near(r["dS0"][0, h], power(T) * dS[0, h].double() + d ** -0.5 * (power(N + 1)[:, None] * qh).T @ oh, f"dS0 {h}")
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+def test_slow_decays_over_many_steps(cuda_device, dk, dv):
+    """20,000 tokens without input.  An element is rounded once a token, 2^-24 of it at most, and the
+    same way for as long as its mantissa hardly moves, so an element may be off by n times that.  But
+    elements round either way: what all of them lose alike, the decay's own error, is that divided by
+    sqrt(3) and the root of their number, five times over, and 2^-23 of every |l| for the decay."""
+    H, n = 4, 20000
+    l = torch.tensor([unlucky(1), unlucky(1, 1e-5, 3e-5), unlucky(1, 1e-4, 3e-4), -2.0 ** -8], device="cuda")
+    S = torch.randn(2, H, dk, dv, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    ref = (l.double() * n).exp()[:, None, None] * S.double()
+    zero = torch.zeros(2, H, dk, device="cuda")
+    v, o = torch.ones(2, H, dv, device="cuda"), torch.empty(2, H, dv, device="cuda")
+    for _ in range(n):
+        kda.linear_recurrent_step(zero, zero, v, l, S, o=o)
+    for h in range(H):
+        off, r, own = S[:, h].double() - ref[:, h], ref[:, h], n * abs(float(l[h])) * 2.0 ** -23
+        assert bool((off.abs() <= (n * 2.0 ** -24 + own) * r.abs() + n * 2.0 ** -149).all()), h
+        common = float((off * r).sum() / r.square().sum())
+        assert abs(common) <= 5 * n * 2.0 ** -24 / (3 * r.numel()) ** 0.5 + own, (h, common)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+def test_slow_decays_over_steps_with_input(cuda_device, dk, dv):
+    """5,000 tokens: every one moves each element by a random amount, so its roundings (two a token,
+    2^-24 / sqrt(3) of the state each) are independent; twice what they add up to."""
+    H, n = 2, 5000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    l = torch.tensor([unlucky(1), unlucky(1, 1e-5, 3e-5)], device="cuda")
+    S = 8 * torch.randn(2, H, dk, dv, generator=g, device="cuda")
+    ref, e, o = S.double(), l.double().exp()[:, None, None], torch.empty(2, H, dv, device="cuda")
+    for _ in range(n):
+        k, v = (torch.randn(2, H, d, generator=g, device="cuda") for d in (dk, dv))
+        kda.linear_recurrent_step(k, k, v, l, S, o=o)
+        ref = e * ref + k.double()[..., :, None] * v.double()[..., None, :]
+    for h in range(H):
+        rel = float((S[:, h].double() - ref[:, h]).norm() / ref[:, h].norm())
+        assert rel <= 2 * (2 * n) ** 0.5 * 2.0 ** -24 / 3 ** 0.5, (h, rel)
