@@ -4,7 +4,7 @@
 //   S <- lambda S + k v^T,   o = dk^{-1/2} S^T q
 //
 // The state is read once and written once, 4 dk dv bytes each way per head, and
-// that traffic bounds the step: B=256, H=32 takes 159 us, 6.8 TB/s, 3 % above a plain
+// that traffic bounds the step: B=256, H=32 takes 160 us, 6.8 TB/s, 3 % above a plain
 // copy's rate.  Each thread holds four value columns of ROWS rows, all loaded before
 // the first is used, so the update and the read need no exchange; the column sums are
 // joined across the lanes of a warp that share columns, then across warps.

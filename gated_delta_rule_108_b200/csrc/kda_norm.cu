@@ -12,8 +12,8 @@
 //   dx = r h - m r^3 <h, x> x,   dw = sum over tokens and heads of g r x
 //
 // Both read each row once and write it once: HBM bandwidth bounds them at size (65,536
-// tokens of 32 + 8 heads, d = 128: 226 us in short runs, 91 % of a plain copy's rate, and
-// 242 us, 85 %, at the clock that the power limit leaves in long ones, issue 54 %; the
+// tokens of 32 + 8 heads, d = 128: 225 us in short runs, 91 % of a plain copy's rate, and
+// 240 us, 85 %, at the clock that the power limit leaves in long ones, issue 54 %; the
 // gradients of 4 x 4096 tokens of 16 + 16 heads 82 us, 75 %, and 86 us, 71 %, where the
 // weights' sums hold 128 registers and leave two CTAs an SM), launch latency for a
 // handful of tokens.  A lane holds eight channels of a row, in

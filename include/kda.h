@@ -430,7 +430,8 @@ kda_status kda_linear_recurrent_step(const void* q, const void* k, const void* v
  *  inv_freq    [rotary_dim / 2] fp32 (NULL only with rotary_dim = 0)
  *  positions   [B, T] int32, or NULL for 0 .. T-1 in every row of the batch
  *  d           a multiple of 8 up to 256; rotary_dim a multiple of 16 up to d
- *  eps         > 0: a row of zeros gives zeros
+ *  eps         > 0: a row of zeros gives zeros.  sum x^2 is formed in fp32: a row whose
+ *              sum overflows (elements beyond some 10^18) gives zeros too
  *  q_out       [B, T, Hq, d], k_out [B, T, Hk, d] dtype, contiguous, written; each
  *              may be its (contiguous) input itself, and must not overlap it otherwise,
  *              nor any other of the tensors
